@@ -147,6 +147,13 @@ typedef enum cg_status {
   CG_ERR_UNSUPPORTED = 7  /* shape outside the limits listed above */
 } cg_status;
 
+/* Value type of a pool and of the queries that meet it (the paged serving
+ * calls).  The codec itself is fp16. */
+typedef enum cg_dtype {
+  CG_DTYPE_F16 = 0,
+  CG_DTYPE_BF16 = 1
+} cg_dtype;
+
 typedef struct cg_shape {
   int32_t num_layers;   /* L */
   int32_t num_kv_heads; /* H */
@@ -362,6 +369,151 @@ cg_status cg_encode_static(const cg_shape* shape, const uint16_t* kv_dev, int64_
                            cg_level level, const uint8_t* tables_dev, uint8_t* out_dev,
                            uint64_t out_stride, uint64_t* out_sizes_dev, int32_t* status_dev,
                            cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged serving calls.  A context whose containers cg_decode_into_paged has
+ * decoded into a paged pool is there to be continued: the calls below make the
+ * block tables of a batch, write the keys and values of its new tokens into
+ * the same pool, and attend over it.  The pool is that call's,
+ * [L][2][num_pages][page_tokens][H][D], and a request's row of a block table
+ * is its block_table_dev.  The conventions above hold: the caller owns every
+ * buffer, nothing is allocated or synchronised, everything is ordered on
+ * `stream` and can be captured; argument errors are synchronous, data errors
+ * go to *status_dev.  Row pointers (q, k, v, outputs, weights, pool) are
+ * 16-byte aligned and token strides, in elements, multiples of 8 and at least
+ * the row's heads * D; a token's heads are contiguous.
+ * The arithmetic is fp32; values are rounded to the pool's type when they are
+ * stored (and the weights of a softmax for the matrix product that uses them).
+ * Indexes and lengths are checked on the device before they are used; what a
+ * bad one reaches is left out and CG_ERR_MISMATCH reported. */
+
+/* Arguments of cg_extend_tables. */
+typedef struct cg_extend_args {
+  int32_t num_requests;  /* B, 1 .. 8192 */
+  int32_t page_tokens;   /* P */
+  int32_t num_pages;     /* pages of the pool */
+  int32_t max_pages;     /* entries of a row of block_tables_dev */
+  int32_t num_free;      /* entries of free_pages_dev */
+  int32_t max_tokens;    /* rows of slots_dev and positions_dev */
+  int32_t position_base; /* position of a request's first token (>= 0): the length of a shared
+                            prefix that lies in a table of its own, else 0 */
+  const int32_t* held_dev;       /* [B] tokens each request has in the pool */
+  const int32_t* added_dev;      /* [B] tokens it adds now (0 allowed) */
+  const int32_t* free_pages_dev; /* [num_free] pages in the order they are handed out, each once */
+  const int32_t* taken_dev;      /* [1] entries of free_pages_dev handed out before */
+  int32_t* taken_out_dev;        /* [1] the same after the call */
+  int32_t* block_tables_dev;     /* [B][max_pages], extended in place */
+  int32_t* kv_lens_dev;          /* [B] held + added */
+  int32_t* q_starts_dev;         /* [B + 1] first packed row of each request's new tokens */
+  int64_t* slots_dev;            /* [max_tokens] pool row (page * P + row in page), -1 behind the
+                                    last token */
+  int32_t* positions_dev;        /* [max_tokens] position of each new token, -1 behind the last */
+  int32_t* status_dev;
+} cg_extend_args;
+
+/* Block tables and slot maps of a batch from its lengths, in one launch.  The
+ * new tokens are packed request by request; a request takes a page from the
+ * free list for each page its held + added tokens need beyond the
+ * ceil(held / P) it has, in request order.  taken_out_dev may be taken_dev and
+ * kv_lens_dev may be held_dev.  All or nothing: on a data error (a negative
+ * length, a page outside the pool or a bad `taken`: CG_ERR_MISMATCH; too few
+ * free pages, table entries or rows: CG_ERR_CAPACITY) the tables and the count
+ * stay as they were, kv_lens is held, q_starts is 0 and every slot and position
+ * is -1, so that the calls after it on the stream have no rows. */
+cg_status cg_extend_tables(const cg_extend_args* args, cudaStream_t stream);
+
+/* The table cg_append_qkv turns queries and keys by: row p of out_dev
+ * ([max_positions][rot_dim] fp32) holds cos(p * theta^(-2i / rot_dim)) for
+ * i < rot_dim / 2, then the sines, computed in 64 bits.  rot_dim is even. */
+cg_status cg_rope_table(int32_t max_positions, int32_t rot_dim, double theta, float* out_dev,
+                        cudaStream_t stream);
+
+/* Arguments of cg_append_qkv. */
+typedef struct cg_append_args {
+  int32_t num_tokens;  /* packed rows of q, k, v */
+  int32_t num_q_heads; /* Hq */
+  int32_t layer;       /* layer of the pool that is written */
+  int32_t num_pages;
+  int32_t page_tokens;
+  int32_t max_positions; /* rows of rope_dev */
+  int32_t rot_dim;       /* leading channels of a head that are turned: even, 0 .. D */
+  int32_t interleaved;   /* pairs (2i, 2i + 1) if not 0, else (i, i + rot_dim / 2) */
+  cg_dtype dtype;
+  float eps;
+  const uint16_t* q_dev; /* [num_tokens] rows of Hq * D at q_stride */
+  const uint16_t* k_dev; /* H * D at k_stride */
+  const uint16_t* v_dev; /* H * D at v_stride */
+  int64_t q_stride, k_stride, v_stride;
+  uint16_t* q_out_dev;   /* may be q_dev (with the same stride) */
+  int64_t q_out_stride;
+  const uint16_t* q_weight_dev; /* [D] norm weights, or NULL: no norm */
+  const uint16_t* k_weight_dev;
+  const float* rope_dev;          /* cg_rope_table's layout; NULL if rot_dim is 0 */
+  const int32_t* positions_dev;   /* [num_tokens]; NULL if rot_dim is 0 */
+  const int64_t* slots_dev;       /* [num_tokens] */
+  uint16_t* pool_dev;
+  int32_t* status_dev;
+} cg_append_args;
+
+/* For each token and head: y = x * rsqrt(mean(x^2) + eps) * weight (queries and
+ * keys, where a weight is given), then the rotation (y_a, y_b) -> (y_a c - y_b s,
+ * y_b c + y_a s) of its position; queries go to q_out_dev, keys and values to
+ * row slots_dev[t] of the layer's halves of the pool.  A token with a negative
+ * slot is left out (its rows and the pool stay as they were).  Two tokens of a
+ * call must not have the same slot: the row would hold parts of both. */
+cg_status cg_append_qkv(const cg_shape* shape, const cg_append_args* args, cudaStream_t stream);
+
+/* Arguments of cg_attention_paged and cg_attention_shared. */
+typedef struct cg_attention_args {
+  int32_t num_requests; /* B, 1 .. 8192 */
+  int32_t num_tokens;   /* rows of q and out (those behind q_starts[B] are left as they were) */
+  int32_t max_q;        /* no request has more new tokens than this */
+  int32_t num_q_heads;  /* Hq, a multiple of the shape's H, at most 64 times it */
+  int32_t layer;
+  int32_t num_pages;
+  int32_t page_tokens;
+  int32_t max_pages; /* entries of a row of block_tables_dev */
+  int32_t window;    /* keys a row sees up to its own, 0: all */
+  int32_t sinks;     /* first keys that stay visible behind the window */
+  cg_dtype dtype;
+  float scale; /* of q . k */
+  const uint16_t* q_dev;
+  uint16_t* out_dev; /* must not overlap q */
+  int64_t q_stride, out_stride;
+  float* lse_dev;                  /* [num_tokens][Hq] log of the sum of exp(score), or NULL */
+  const int32_t* q_starts_dev;     /* [B + 1] */
+  const int32_t* kv_lens_dev;      /* [B] tokens in the pool, the new ones included */
+  const int32_t* block_tables_dev; /* [B][max_pages] */
+  const uint16_t* pool_dev;
+  int32_t* status_dev;
+  void* workspace_dev; /* 256-byte aligned; calls that overlap need one each */
+  uint64_t workspace_bytes;
+} cg_attention_args;
+
+/* Device workspace of the attention calls for at most max_tokens rows and
+ * max_requests requests; `shared` for cg_attention_shared.  Needs no clearing.
+ * Host, pure. */
+cg_status cg_attention_workspace_bytes(const cg_shape* shape, int32_t num_q_heads,
+                                       int32_t max_tokens, int32_t max_requests, int32_t shared,
+                                       uint64_t* bytes);
+
+/* Causal attention of each request's new tokens over its tokens in the pool:
+ * new token i of request r stands at position p = kv_len - n + i and sees the
+ * keys j <= p with window == 0, j > p - window or j < sinks.  Query head h
+ * uses kv head h / (Hq / H).  A row that sees nothing gives zeros and a
+ * log-sum of -infinity.  Keys that no row sees are not read. */
+cg_status cg_attention_paged(const cg_shape* shape, const cg_attention_args* args,
+                             cudaStream_t stream);
+
+/* The same (window 0, sinks 0) for a batch whose requests share a prefix of
+ * prefix_tokens tokens that lies in the pool once, in the pages of
+ * prefix_table_dev: every row sees the whole prefix, then its own request's
+ * tokens as above.  The prefix is attended by all rows of the batch together,
+ * so its keys and values are read once and not once a request, and the parts
+ * are joined by their maxima and sums. */
+cg_status cg_attention_shared(const cg_shape* shape, const cg_attention_args* args,
+                              const int32_t* prefix_table_dev, int32_t prefix_tokens,
+                              cudaStream_t stream);
 
 #ifdef __cplusplus
 }

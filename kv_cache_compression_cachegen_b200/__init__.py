@@ -20,10 +20,14 @@ __all__ = [
     "cg_encoded_bound", "cg_tables_bytes", "cg_encode_workspace_bytes", "cg_build_tables",
     "cg_encode", "cg_encode_static", "cg_encode_levels", "cg_encode_levels_workspace_bytes",
     "cg_encode_adjacent", "cg_decode_adjacent", "cg_decode_adjacent_into", "cg_decode_adjacent_into_paged", "cg_decode", "cg_decode_into", "cg_decode_into_paged",
+    "CG_DTYPE_F16", "CG_DTYPE_BF16", "ExtendArgs", "AppendArgs", "AttentionArgs",
+    "cg_extend_tables", "cg_rope_table", "cg_append_qkv", "cg_attention_workspace_bytes",
+    "cg_attention_paged", "cg_attention_shared",
 ]
 
 CG_OK, CG_ERR_INVALID_ARG, CG_ERR_CAPACITY, CG_ERR_CORRUPT = 0, 1, 2, 3
 CG_ERR_MISMATCH, CG_ERR_NONFINITE, CG_ERR_CUDA, CG_ERR_UNSUPPORTED = 4, 5, 6, 7
+CG_DTYPE_F16, CG_DTYPE_BF16 = 0, 1
 LEVELS = {"high": 0, "balanced": 1, "fast": 2}
 
 _PKG = Path(__file__).resolve().parent
@@ -53,6 +57,41 @@ class Shape(ctypes.Structure):
 
 
 _P = ctypes.c_void_p
+_I32, _I64, _F32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class ExtendArgs(ctypes.Structure):
+    """cg_extend_args (include/cachegen.h documents every field)."""
+    _fields_ = ([(n, _I32) for n in ("num_requests", "page_tokens", "num_pages", "max_pages",
+                                     "num_free", "max_tokens", "position_base")]
+                + [(n, _P) for n in ("held", "added", "free_pages", "taken", "taken_out",
+                                     "block_tables", "kv_lens", "q_starts", "slots", "positions",
+                                     "status")])
+
+
+class AppendArgs(ctypes.Structure):
+    """cg_append_args."""
+    _fields_ = ([(n, _I32) for n in ("num_tokens", "num_q_heads", "layer", "num_pages",
+                                     "page_tokens", "max_positions", "rot_dim", "interleaved",
+                                     "dtype")]
+                + [("eps", _F32), ("q", _P), ("k", _P), ("v", _P), ("q_stride", _I64),
+                   ("k_stride", _I64), ("v_stride", _I64), ("q_out", _P), ("q_out_stride", _I64)]
+                + [(n, _P) for n in ("q_weight", "k_weight", "rope", "positions", "slots", "pool",
+                                     "status")])
+
+
+class AttentionArgs(ctypes.Structure):
+    """cg_attention_args."""
+    _fields_ = ([(n, _I32) for n in ("num_requests", "num_tokens", "max_q", "num_q_heads", "layer",
+                                     "num_pages", "page_tokens", "max_pages", "window", "sinks",
+                                     "dtype")]
+                + [("scale", _F32), ("q", _P), ("out", _P), ("q_stride", _I64),
+                   ("out_stride", _I64)]
+                + [(n, _P) for n in ("lse", "q_starts", "kv_lens", "block_tables", "pool",
+                                     "status", "workspace")]
+                + [("workspace_bytes", ctypes.c_uint64)])
+
+
 _SIGNATURES = {
     "cg_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "cg_section_offsets": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32,
@@ -101,6 +140,17 @@ _SIGNATURES = {
                                                      ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
                                                      _P, ctypes.c_int32, ctypes.c_int32, _P,
                                                      ctypes.c_int64, _P, _P]),
+    "cg_extend_tables": (ctypes.c_int, [ctypes.POINTER(ExtendArgs), _P]),
+    "cg_rope_table": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_double, _P, _P]),
+    "cg_append_qkv": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.POINTER(AppendArgs), _P]),
+    "cg_attention_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32,
+                                                    ctypes.c_int32, ctypes.c_int32,
+                                                    ctypes.c_int32,
+                                                    ctypes.POINTER(ctypes.c_uint64)]),
+    "cg_attention_paged": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.POINTER(AttentionArgs),
+                                          _P]),
+    "cg_attention_shared": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.POINTER(AttentionArgs),
+                                           _P, ctypes.c_int32, _P]),
 }
 
 _lib = None
@@ -280,3 +330,35 @@ def cg_decode_adjacent_into_paged(shape, inp, in_stride: int, num_chunks: int,
         ctypes.byref(_shape(shape)), _ptr(inp), in_stride, num_chunks, chunk_tokens, int(level),
         _ptr(pool), num_pages, page_tokens, _ptr(block_table), total_tokens, _ptr(status),
         _stream(stream))
+
+
+def cg_extend_tables(args: ExtendArgs, stream=None) -> int:
+    """Block tables and slot maps of a batch from its lengths."""
+    return library().cg_extend_tables(ctypes.byref(args), _stream(stream))
+
+
+def cg_rope_table(max_positions: int, rot_dim: int, theta: float, out, stream=None) -> int:
+    return library().cg_rope_table(max_positions, rot_dim, theta, _ptr(out), _stream(stream))
+
+
+def cg_append_qkv(shape, args: AppendArgs, stream=None) -> int:
+    """Norm and rotate queries and keys; write keys and values into the paged pool."""
+    return library().cg_append_qkv(ctypes.byref(_shape(shape)), ctypes.byref(args),
+                                   _stream(stream))
+
+
+def cg_attention_workspace_bytes(shape, num_q_heads: int, max_tokens: int, max_requests: int,
+                                 shared: bool = False) -> int:
+    return _size_query("cg_attention_workspace_bytes", ctypes.byref(_shape(shape)), num_q_heads,
+                       max_tokens, max_requests, int(shared))
+
+
+def cg_attention_paged(shape, args: AttentionArgs, stream=None) -> int:
+    return library().cg_attention_paged(ctypes.byref(_shape(shape)), ctypes.byref(args),
+                                        _stream(stream))
+
+
+def cg_attention_shared(shape, args: AttentionArgs, prefix_table, prefix_tokens: int,
+                        stream=None) -> int:
+    return library().cg_attention_shared(ctypes.byref(_shape(shape)), ctypes.byref(args),
+                                         _ptr(prefix_table), prefix_tokens, _stream(stream))

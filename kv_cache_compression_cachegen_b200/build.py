@@ -22,12 +22,13 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # uses explicit IEEE round-to-nearest intrinsics as well).
 NVCC_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17", "-fmad=false",
-    "-Xcompiler", "-fPIC,-O2", "-shared",
+    "-Xcompiler", "-fPIC,-O2", "-shared", "--threads", "0",
 ]
 
 CODEC_SOURCES = ["csrc/capi.cu", "csrc/encode.cu", "csrc/decode.cu", "csrc/static_ws.cu",
-                 "csrc/context.cu"]
-CODEC_HEADERS = ["csrc/cg_common.cuh"]
+                 "csrc/context.cu", "csrc/capi_paged.cu", "csrc/tables.cu", "csrc/append.cu",
+                 "csrc/attend.cu"]
+CODEC_HEADERS = ["csrc/cg_common.cuh", "csrc/paged.cuh", "csrc/attend.cuh"]
 SYNTH_SOURCES = ["synth/kvsynth.cu"]
 
 LIB_CODEC = PKG / "libcachegen.so"

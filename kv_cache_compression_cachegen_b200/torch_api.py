@@ -4,7 +4,9 @@ These helpers only allocate device buffers with torch and call the C ABI; the
 codec itself runs entirely in the library's kernels.  KV tensors hold fp16
 bits in a 16-bit dtype (torch.float16 or torch.int16), shaped [L, 2, T, H, D].
 Nothing here synchronises: results are device tensors plus a device status
-word, which the caller checks after synchronising (``status_of``).
+word, which the caller checks after synchronising (``status_of``).  The paged
+serving calls (block tables, append, attention) are in ``paged`` and are
+re-exported here.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ from . import (CG_OK, CacheGenError, Shape, cg_build_tables, cg_decode, cg_decod
                cg_decode_into_paged, cg_encode, cg_encode_adjacent, cg_encode_levels,
                cg_encode_levels_workspace_bytes, cg_encode_workspace_bytes, cg_encoded_bound,
                cg_tables_bytes, check)
+from .paged import PagedAppend, PagedAttention, PagedTables, rope_table  # noqa: F401
 
 
 def _shape_of(kv: torch.Tensor) -> tuple[Shape, int]:
