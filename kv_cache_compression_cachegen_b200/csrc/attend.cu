@@ -17,92 +17,30 @@
 // Each warp takes 16 keys of a unit, keeps its own maximum, sum and output,
 // and the four warps of a CTA are joined once per item.
 #include <algorithm>
+#include <cmath>
 
 #include "attend.cuh"
 
 namespace cg {
 namespace {
 
-constexpr int kRowTile = 16;   // query rows of an item (one matrix tile)
 constexpr int kRowWarps = 4;
-constexpr int kRowKeys = 16 * kRowWarps;  // keys of a unit
+static_assert(kRowKeys == 16 * kRowWarps, "each warp takes 16 keys of a unit");
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kMaxRowCtas = 160 * 4;
-constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kMaxTileCtas = 160;
 
-struct Item {
-  Request req;
-  Span span;
-  int row, rows;   // first row of the tile among the request's rows, rows in it
-  int tokens0;     // first token of the tile
-  bool prefix;
-};
-
-// Slots: request r's tiles start at slot floor(first row / 16) + r, which leaves
-// room for every tile whatever the lengths; slots that hold no tile cost nothing.
-__device__ __forceinline__ int num_slots(const AttnParams& p) {
-  return int(int64_t(p.num_tokens) * p.group / kRowTile) + p.num_requests;
-}
-
-__device__ __forceinline__ int slot_base(const AttnParams& p, int r) {
-  int a = p.q_starts[r];
-  a = a < 0 ? 0 : (a > p.num_tokens ? p.num_tokens : a);
-  return int(int64_t(a) * p.group / kRowTile) + r;
-}
-
-// Units of slot x (for each kv head); 0 where it holds no rows.
-__device__ int slot_item(const AttnParams& p, int x, Item& it) {
-  const int slots = num_slots(p);
-  it.prefix = x >= slots;
-  if (it.prefix) {
-    int n = p.q_starts[p.num_requests];
-    n = n < 0 ? 0 : (n > p.num_tokens ? p.num_tokens : n);
-    it.req.first = 0;
-    it.req.tokens = n;
-    it.req.keys = p.prefix_tokens;
-    it.req.row0 = p.prefix_tokens;  // every row stands behind the prefix
-    it.row = (x - slots) * kRowTile;
-  } else {
-    int lo = 0, hi = p.num_requests - 1;  // the last request whose slots start at or before x
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (slot_base(p, mid) <= x) lo = mid;
-      else hi = mid - 1;
-    }
-    if (!load_request(p, lo, it.req)) {
-      report(p.status, CG_ERR_MISMATCH);
-      return 0;
-    }
-    it.row = (x - slot_base(p, lo)) * kRowTile;
-  }
-  const int rows = it.req.tokens * p.group;
-  if (it.row < 0 || it.row >= rows) return 0;
-  it.rows = rows - it.row < kRowTile ? rows - it.row : kRowTile;
-  if (it.prefix) {
-    it.span = span_of<kRowKeys>(p.prefix_tokens - 1, p.prefix_tokens - 1, 0, 0);
-  } else {
-    const int t0 = div_of(it.row, p.group_div), t1 = div_of(it.row + it.rows - 1, p.group_div);
-    it.span = span_of<kRowKeys>(it.req.row0 + t0, it.req.row0 + t1, p.window, p.sinks);
-  }
-  // an item without a visible key still has its rows to write
-  return it.span.units > 0 ? it.span.units : 1;
-}
-
-__device__ __forceinline__ int total_slots(const AttnParams& p) {
-  return num_slots(p) +
-         (p.shared ? int((int64_t(p.num_tokens) * p.group + kRowTile - 1) / kRowTile) : 0);
-}
-
-// Fill row_cum: units of one head before each slot.  One block.
-__global__ void __launch_bounds__(1024) plan_kernel(AttnParams p) {
+// Units of one head before each slot of a line.  One block.
+template <int kTile, int kKeys>
+__device__ void plan_line(const AttnParams& p, int64_t* cum) {
   __shared__ int64_t warp_sum[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int slots = total_slots(p);
+  const int slots = total_slots<kTile>(p);
   int64_t base = 0;
   for (int x0 = 0; x0 < slots; x0 += 1024) {
     const int x = x0 + threadIdx.x;
     Item it;
-    int64_t own = x < slots ? slot_item(p, x, it) : 0, sum = own;
+    int64_t own = x < slots ? slot_item<kTile, kKeys>(p, x, it) : 0, sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(~0u, sum, o);
@@ -117,27 +55,18 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnParams p) {
       if (lane >= o) wi += up;
     }
     const int64_t before = base + __shfl_sync(~0u, wi - w, warp) + sum - own;
-    if (x < slots) p.row_cum[x] = before;
+    if (x < slots) cum[x] = before;
     base += __shfl_sync(~0u, wi, 31);
     __syncthreads();
   }
-  if (threadIdx.x == 0) p.row_cum[slots] = base;
+  if (threadIdx.x == 0) cum[slots] = base;
 }
 
-// CTAs that get a share: no share is empty.
-__device__ __forceinline__ int shares_of(const AttnParams& p, int64_t units) {
-  return units < p.row_ctas ? int(units) : p.row_ctas;
-}
-
-// Row of the pool that holds a key, or -1 where the table has no such page.
-__device__ __forceinline__ int pool_row(const AttnParams& p, const int32_t* table, int key) {
-  const int col = div_of(key, p.page_div);
-  const int page = __ldg(table + col);
-  if (page < 0 || page >= p.num_pages) {
-    report(p.status, CG_ERR_MISMATCH);
-    return -1;
-  }
-  return page * p.page_tokens + (key - col * p.page_tokens);
+// Block 0 plans the rows kernel, block 1 the tile kernel.
+template <int kTile, int kKeys>
+__global__ void __launch_bounds__(1024) plan_kernel(AttnParams p) {
+  if (blockIdx.x == 0) plan_line<kRowTile, kRowKeys>(p, p.rows.cum);
+  else plan_line<kTile, kKeys>(p, p.tiles.cum);
 }
 
 // DB: 32-channel blocks of a head (K), VB: 64-channel blocks (V).
@@ -148,41 +77,12 @@ __global__ void __launch_bounds__(kRowThreads, DB <= 4 ? 3 : 1) rows_kernel(Attn
   __shared__ float stat_m[kRowWarps][16], stat_l[kRowWarps][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int slots = total_slots(p), H = p.kv_heads, D = p.dim;
-  const int64_t per_head = p.row_cum[slots];
-  const int64_t units = per_head * H;
-  if (units == 0) return;
-  const int ctas = shares_of(p, units);
-  if (int(blockIdx.x) >= ctas) return;
-  int64_t u = units * blockIdx.x / ctas;
-  const int64_t u_end = units * (blockIdx.x + 1) / ctas;
-  const int64_t share0 = u;
-
-  int x = 0;  // the slot that holds unit u: the last one with H * row_cum[x] <= u
-  {
-    int hi = slots - 1;
-    while (x < hi) {
-      const int mid = (x + hi + 1) >> 1;
-      if (p.row_cum[mid] * H <= u) x = mid;
-      else hi = mid - 1;
-    }
-  }
-  int64_t cum = p.row_cum[x];
-
-  while (u < u_end && x < slots) {
-    Item it;
-    const int cost = slot_item(p, x, it);
-    if (cost == 0 || u >= (cum + cost) * H) {
-      cum += cost;
-      ++x;
-      continue;
-    }
-    const int head = int((u - cum * H) / cost);
-    const int64_t item0 = cum * H + int64_t(head) * cost;
-    const int first = int(u - item0);
-    const int last = int((item0 + cost < u_end ? item0 + cost : u_end) - item0);
-    const bool whole = first == 0 && last == cost;
-
+  const int H = p.kv_heads, D = p.dim;
+  Walk<kRowTile, kRowKeys> w;
+  if (!w.begin(p, p.rows)) return;
+  while (w.next(p)) {
+    const Item& it = w.it;
+    const int head = w.head;
     // The two query rows of this lane's quad and their positions.
     uint32_t qf[DB][2][4];
     int pos[2];
@@ -191,34 +91,25 @@ __global__ void __launch_bounds__(kRowThreads, DB <= 4 ? 3 : 1) rows_kernel(Attn
       const int row = it.row + g + 8 * i;
       const int tok = div_of(row, p.group_div);
       const bool real = g + 8 * i < it.rows;
-      pos[i] = it.prefix ? it.req.keys : it.req.row0 + tok;
+      pos[i] = row_position(p, it, row);
       const uint16_t* src = p.q + int64_t(it.req.first + tok) * p.q_stride +
                             int64_t(head * p.group + (row - tok * p.group)) * D;
 #pragma unroll
       for (int b = 0; b < DB; ++b) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (real && 32 * b + 8 * c < D) v = *reinterpret_cast<const uint4*>(src + 32 * b + 8 * c);
-        qf[b][0][i] = v.x;
-        qf[b][0][2 + i] = v.y;
-        qf[b][1][i] = v.z;
-        qf[b][1][2 + i] = v.w;
+        qf[b][0][i] = v.x ^ p.q_flip;
+        qf[b][0][2 + i] = v.y ^ p.q_flip;
+        qf[b][1][i] = v.z ^ p.q_flip;
+        qf[b][1][2 + i] = v.w ^ p.q_flip;
       }
     }
-    const int32_t* table = it.prefix ? p.prefix_table : nullptr;
-    if (!it.prefix) {
-      // the request of the slot: found again from its first row
-      int lo = 0, hi = p.num_requests - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (slot_base(p, mid) <= x) lo = mid;
-        else hi = mid - 1;
-      }
-      table = p.tables + int64_t(lo) * p.max_pages;
-    }
+    const bool prefix = it.request < 0;
+    const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
     const uint16_t* kb = p.k_pool + int64_t(head) * D;
     const uint16_t* vb = p.v_pool + int64_t(head) * D;
     const int64_t step = int64_t(H) * D;
-    const int window = it.prefix ? 0 : p.window, sinks = it.prefix ? 0 : p.sinks;
+    const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
     const int tok0 = div_of(it.row, p.group_div);
     const int tok1 = div_of(it.row + it.rows - 1, p.group_div);
 
@@ -231,7 +122,7 @@ __global__ void __launch_bounds__(kRowThreads, DB <= 4 ? 3 : 1) rows_kernel(Attn
         for (int e = 0; e < 4; ++e) acc[b][j][e] = 0.f;
     float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};  // m in log2 units
 
-    for (int unit = first; unit < last && it.span.units > 0; ++unit) {
+    for (int unit = w.first; unit < w.last; ++unit) {
       const int key0 = unit_key<kRowKeys>(it.span, unit) + 16 * warp;
       int mine = -1;  // pool row of key0 + (lane & 15); -1: no row of the tile sees it
       {
@@ -382,7 +273,7 @@ __global__ void __launch_bounds__(kRowThreads, DB <= 4 ? 3 : 1) rows_kernel(Attn
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float top = kNegInf;
-      for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, stat_m[w][g + 8 * i]);
+      for (int k = 0; k < kRowWarps; ++k) top = fmaxf(top, stat_m[k][g + 8 * i]);
       const float f = weight_of(m[i], top);
       // this lane has channels 64 b + 16 c + 0 .. 15 of its rows
       float* dst = smem + (warp * 16 + g + 8 * i) * (VB * 64) + 16 * c;
@@ -397,42 +288,72 @@ __global__ void __launch_bounds__(kRowThreads, DB <= 4 ? 3 : 1) rows_kernel(Attn
     __syncthreads();
     // Thread: four channels of a row at a time.
     const int quads = D / 4;
-    const int piece = 2 * int(blockIdx.x) + (item0 >= share0 ? 1 : 0);
     for (int i = threadIdx.x; i < it.rows * quads; i += kRowThreads) {
       const int row = i / quads, d = (i - row * quads) * 4;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < kRowWarps; ++w) {
-        const float4 v = *reinterpret_cast<const float4*>(smem + (w * 16 + row) * (VB * 64) + d);
+      for (int k = 0; k < kRowWarps; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(smem + (k * 16 + row) * (VB * 64) + d);
         o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
       }
       float mm = kNegInf, ll = 0.f;
-      for (int w = 0; w < kRowWarps; ++w) mm = fmaxf(mm, stat_m[w][row]);
-      for (int w = 0; w < kRowWarps; ++w) ll += stat_l[w][row] * weight_of(stat_m[w][row], mm);
+      for (int k = 0; k < kRowWarps; ++k) mm = fmaxf(mm, stat_m[k][row]);
+      for (int k = 0; k < kRowWarps; ++k) ll += stat_l[k][row] * weight_of(stat_m[k][row], mm);
       const int tok = div_of(it.row + row, p.group_div);
       const int64_t t = it.req.first + tok;
       const int qh = head * p.group + it.row + row - tok * p.group;
-      if (!whole) {
-        *reinterpret_cast<float4*>(p.row_pieces + (int64_t(piece) * kRowTile + row) * D + d) = o;
-        if (d == 0) p.row_stats[piece * kRowTile + row] = make_float2(mm, ll);
+      if (!w.whole) {
+        const int64_t at = int64_t(w.piece) * kRowTile + row;
+        *reinterpret_cast<float4*>(p.rows.pieces + at * D + d) = o;
+        if (d == 0) p.rows.stats[at] = make_float2(mm, ll);
       } else if (p.shared) {
-        const int64_t at = (int64_t(it.prefix) * p.num_tokens + t) * p.q_heads + qh;
+        const int64_t at = (int64_t(prefix) * p.num_tokens + t) * p.q_heads + qh;
         *reinterpret_cast<float4*>(p.whole + at * D + d) = o;
         if (d == 0) p.whole_stats[at] = make_float2(mm, ll);
       } else {
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         *reinterpret_cast<uint2*>(p.out + t * p.out_stride + int64_t(qh) * D + d) =
             make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv));
-        if (d == 0 && p.lse != nullptr)
-          p.lse[t * p.q_heads + qh] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * 0.69314718056f;
+        if (d == 0 && p.lse != nullptr) p.lse[t * p.q_heads + qh] = log_sum(mm, ll);
       }
     }
     __syncthreads();  // smem is written again
-    u = item0 + last;
   }
 }
 
+// Where the parts of one row of a line lie.
+struct Part {
+  int c0, c1, in_tile;  // CTAs that hold units of the row's item; the row in the tile
+  int64_t item0, units, whole_at;
+  int ctas;
+  const Lane* lane;
+
+  template <int kTile>
+  __device__ void find(const AttnParams& p, const Lane& l, bool prefix, int request, int row,
+                       int head) {
+    lane = &l;
+    const int x = (prefix ? own_slots<kTile>(p) : slot_base<kTile>(p, request)) + row / kTile;
+    in_tile = row % kTile;
+    const int64_t cost = l.cum[x + 1] - l.cum[x];
+    units = l.cum[total_slots<kTile>(p)] * p.kv_heads;
+    ctas = shares_of(l, units);
+    item0 = l.cum[x] * p.kv_heads + head * cost;
+    c0 = cta_of(item0, units, ctas);
+    c1 = cta_of(item0 + cost - 1, units, ctas);
+  }
+  __device__ bool whole() const { return c0 == c1; }
+  __device__ int64_t at(int cta) const {
+    return int64_t(2 * cta + (item0 >= units * cta / ctas ? 1 : 0)) * lane->tile + in_tile;
+  }
+  __device__ float2 stat(const AttnParams& p, int cta) const {
+    return whole() ? p.whole_stats[whole_at] : lane->stats[at(cta)];
+  }
+  __device__ const float* values(const AttnParams& p, int cta) const {
+    return whole() ? p.whole + whole_at * p.dim : lane->pieces + at(cta) * p.dim;
+  }
+};
+
 // One warp joins one (token, query head) row from its pieces.
-template <typename T>
+template <typename T, int kDim>
 __global__ void __launch_bounds__(256) join_kernel(AttnParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t row_id = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -449,47 +370,33 @@ __global__ void __launch_bounds__(256) join_kernel(AttnParams p) {
   Request req;
   if (!load_request(p, lo, req) || t < req.first || t >= req.first + req.tokens) return;
 
-  const int slots = total_slots(p), H = p.kv_heads, D = p.dim;
-  const int64_t units = p.row_cum[slots] * H;
-  const int ctas = shares_of(p, units);
-  // the pieces of the row's own item, and of its prefix item
-  int c0[2] = {0, 0}, c1[2] = {-1, -1}, in_tile[2] = {0, 0};
-  int64_t item0[2] = {0, 0};
-  bool whole[2] = {false, false};
-  for (int k = 0; k < (p.shared ? 2 : 1); ++k) {
+  const int D = p.dim;
+  // the parts of the row: its own item's, and its prefix item's
+  Part part[2];
+  const int parts = p.shared ? 2 : 1;
+  for (int k = 0; k < parts; ++k) {
     const int row = (k ? t : t - req.first) * p.group + member;
-    const int x = (k ? num_slots(p) : slot_base(p, lo)) + row / kRowTile;
-    in_tile[k] = row % kRowTile;
-    const int64_t cost = p.row_cum[x + 1] - p.row_cum[x];
-    item0[k] = p.row_cum[x] * H + head * cost;
-    c0[k] = cta_of(item0[k], units, ctas);
-    c1[k] = cta_of(item0[k] + cost - 1, units, ctas);
-    whole[k] = c0[k] == c1[k];
+    const bool small = k ? p.prefix_small != 0 : req.tokens * p.group <= kRowTile;
+    if (small) part[k].find<kRowTile>(p, p.rows, k != 0, lo, row, head);
+    else if (kDim <= 128) part[k].find<256>(p, p.tiles, k != 0, lo, row, head);
+    else part[k].find<128>(p, p.tiles, k != 0, lo, row, head);
+    part[k].whole_at = int64_t(k) * p.num_tokens * p.q_heads + row_id;
   }
-  if (!p.shared && whole[0]) return;  // written by the CTA that had all of it
+  if (!p.shared && part[0].whole()) return;  // written by the CTA that had all of it
 
   float mm = kNegInf;
-  const auto at_piece = [&](int k, int cta) -> int64_t {
-    const int64_t share0 = units * cta / ctas;
-    return int64_t(2 * cta + (item0[k] >= share0 ? 1 : 0)) * kRowTile + in_tile[k];
-  };
-  const auto stat = [&](int k, int cta) -> float2 {
-    return whole[k] ? p.whole_stats[int64_t(k) * p.num_tokens * p.q_heads + row_id]
-                    : p.row_stats[at_piece(k, cta)];
-  };
-  for (int k = 0; k < 2; ++k)
-    for (int cta = c0[k]; cta <= c1[k]; ++cta) mm = fmaxf(mm, stat(k, cta).x);
+  for (int k = 0; k < parts; ++k)
+    for (int cta = part[k].c0; cta <= part[k].c1; ++cta) mm = fmaxf(mm, part[k].stat(p, cta).x);
   float ll = 0.f;
   float4 o[2];  // channels 4 * lane and 128 + 4 * lane
 #pragma unroll
   for (int h = 0; h < 2; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = 0; k < 2; ++k)
-    for (int cta = c0[k]; cta <= c1[k]; ++cta) {
-      const float2 st = stat(k, cta);
+  for (int k = 0; k < parts; ++k)
+    for (int cta = part[k].c0; cta <= part[k].c1; ++cta) {
+      const float2 st = part[k].stat(p, cta);
       const float f = weight_of(st.x, mm);
       ll += st.y * f;
-      const float* src = whole[k] ? p.whole + (int64_t(k) * p.num_tokens * p.q_heads + row_id) * D
-                                  : p.row_pieces + at_piece(k, cta) * D;
+      const float* src = part[k].values(p, cta);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (128 * h + 4 * lane < D) {
@@ -505,26 +412,40 @@ __global__ void __launch_bounds__(256) join_kernel(AttnParams p) {
                                 4 * lane) =
           make_uint2(T::pack(o[h].x * inv, o[h].y * inv), T::pack(o[h].z * inv, o[h].w * inv));
   if (lane == 0 && p.lse != nullptr)
-    p.lse[row_id] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * 0.69314718056f;
+    p.lse[row_id] = log_sum(mm, ll);
 }
 
 uint64_t up256(uint64_t v) { return (v + 255) & ~uint64_t(255); }
 
 struct Workspace {
-  uint64_t row_cum, row_pieces, row_stats, whole, whole_stats, total;
+  uint64_t row_cum, row_pieces, row_stats, tile_cum, tile_pieces, tile_stats, whole, whole_stats,
+      total;
 };
 
 Workspace workspace_of(const cg_shape& s, int Hq, int tokens, int requests, bool shared) {
   const uint64_t D = s.head_dim, group = Hq / s.num_kv_heads;
-  const uint64_t slots = 2 * (tokens * group / kRowTile) + requests + 1;
-  Workspace w;
-  w.row_cum = 0;
-  w.row_pieces = up256(w.row_cum + (slots + 1) * 8);
-  w.row_stats = up256(w.row_pieces + uint64_t(2) * kMaxRowCtas * kRowTile * D * 4);
-  w.whole = up256(w.row_stats + uint64_t(2) * kMaxRowCtas * kRowTile * 8);
+  const uint64_t tile = tile_rows(s.head_dim);
+  const uint64_t row_slots = uint64_t(requests) + 1;
+  const uint64_t tile_slots = 2 * (tokens * group / tile) + requests + 1;
+  // without a request or a batch of more than 16 rows the tile kernel has no work
+  const uint64_t tile_ctas = tokens * group > kRowTile ? kMaxTileCtas : 0;
   const uint64_t rows = shared ? uint64_t(2) * tokens * Hq : 0;
-  w.whole_stats = up256(w.whole + rows * D * 4);
-  w.total = up256(w.whole_stats + rows * 8);
+  Workspace w;
+  uint64_t at = 0;
+  const auto take = [&at](uint64_t bytes) {
+    const uint64_t here = at;
+    at = up256(at + bytes);
+    return here;
+  };
+  w.row_cum = take((row_slots + 1) * 8);
+  w.row_pieces = take(uint64_t(2) * kMaxRowCtas * kRowTile * D * 4);
+  w.row_stats = take(uint64_t(2) * kMaxRowCtas * kRowTile * 8);
+  w.tile_cum = take((tile_slots + 1) * 8);
+  w.tile_pieces = take(2 * tile_ctas * tile * D * 4);
+  w.tile_stats = take(2 * tile_ctas * tile * 8);
+  w.whole = take(rows * D * 4);
+  w.whole_stats = take(rows * 8);
+  w.total = at;
   return w;
 }
 
@@ -536,21 +457,29 @@ cudaError_t launch_rows(const AttnParams& p, cudaStream_t stream) {
         rows_kernel<T, DB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
   }
-  rows_kernel<T, DB><<<p.row_ctas, kRowThreads, smem, stream>>>(p);
+  rows_kernel<T, DB><<<p.rows.ctas, kRowThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_type(AttnParams& p, int sms, cudaStream_t stream) {
-  p.row_ctas = std::min(kMaxRowCtas, sms * (p.dim <= 128 ? 3 : 1));
-  plan_kernel<<<1, 1024, 0, stream>>>(p);
+cudaError_t launch_type(AttnParams& p, int sms, bool bf16, cudaStream_t stream) {
+  p.rows.ctas = std::min(kMaxRowCtas, sms * (p.dim <= 128 ? 3 : 1));
+  p.rows.tile = kRowTile;
+  p.tiles.tile = tile_rows(p.dim);
+  const bool tiles = p.tiled || (p.shared && !p.prefix_small);
+  p.tiles.ctas = tiles ? std::min(kMaxTileCtas, sms) : 0;
+  if (p.dim <= 128) plan_kernel<256, 128><<<tiles ? 2 : 1, 1024, 0, stream>>>(p);
+  else plan_kernel<128, 64><<<tiles ? 2 : 1, 1024, 0, stream>>>(p);
   cudaError_t err = cudaGetLastError();
+  if (err == cudaSuccess && tiles) err = launch_tiles(p, bf16, stream);
   if (err == cudaSuccess)
     err = p.dim <= 64 ? launch_rows<T, 2>(p, stream)
                       : (p.dim <= 128 ? launch_rows<T, 4>(p, stream) : launch_rows<T, 8>(p, stream));
   if (err != cudaSuccess) return err;
   const int64_t rows = int64_t(p.num_tokens) * p.q_heads;
-  join_kernel<T><<<unsigned((rows + 7) / 8), 256, 0, stream>>>(p);
+  const unsigned grid = unsigned((rows + 7) / 8);
+  if (p.dim <= 128) join_kernel<T, 128><<<grid, 256, 0, stream>>>(p);
+  else join_kernel<T, 256><<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -599,16 +528,24 @@ cudaError_t launch_attention(const cg_attention_args& a, const cg_shape& s,
   p.sinks = a.sinks;
   p.prefix_tokens = prefix_tokens;
   p.shared = shared;
-  p.scale_log2 = a.scale * 1.44269504089f;
+  // a negative scale is the positive one with q's signs turned, so that the
+  // largest product is the largest score
+  p.scale_log2 = std::fabs(a.scale) * 1.44269504089f;
+  p.q_flip = std::signbit(a.scale) ? 0x80008000u : 0u;
+  p.prefix_small = int64_t(p.num_tokens) * p.group <= kRowTile;
+  p.tiled = int64_t(p.max_q) * p.group > kRowTile && !p.prefix_small;
   uint8_t* w = static_cast<uint8_t*>(a.workspace_dev);
   const Workspace ws = workspace_of(s, a.num_q_heads, a.num_tokens, a.num_requests, shared);
-  p.row_cum = reinterpret_cast<int64_t*>(w + ws.row_cum);
-  p.row_pieces = reinterpret_cast<float*>(w + ws.row_pieces);
-  p.row_stats = reinterpret_cast<float2*>(w + ws.row_stats);
+  p.rows.cum = reinterpret_cast<int64_t*>(w + ws.row_cum);
+  p.rows.pieces = reinterpret_cast<float*>(w + ws.row_pieces);
+  p.rows.stats = reinterpret_cast<float2*>(w + ws.row_stats);
+  p.tiles.cum = reinterpret_cast<int64_t*>(w + ws.tile_cum);
+  p.tiles.pieces = reinterpret_cast<float*>(w + ws.tile_pieces);
+  p.tiles.stats = reinterpret_cast<float2*>(w + ws.tile_stats);
   p.whole = reinterpret_cast<float*>(w + ws.whole);
   p.whole_stats = reinterpret_cast<float2*>(w + ws.whole_stats);
-  return a.dtype == CG_DTYPE_F16 ? launch_type<F16>(p, sms, stream)
-                                 : launch_type<BF16>(p, sms, stream);
+  return a.dtype == CG_DTYPE_F16 ? launch_type<F16>(p, sms, false, stream)
+                                 : launch_type<BF16>(p, sms, true, stream);
 }
 
 }  // namespace cg

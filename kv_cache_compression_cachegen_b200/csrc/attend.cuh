@@ -1,11 +1,16 @@
 // attend.cuh -- what the attention kernels share: their parameters, which
 // keys a request's rows see, and how the work is dealt to the CTAs.
 //
+// Two kernels.  Requests with at most 16 query rows a kv head (tokens times
+// heads of a group: single tokens, a few at most) are bound by the bytes of K
+// and V and go to the rows kernel; the others, and a shared prefix under the
+// rows of a whole batch, are matrix products and go to the tile kernel.
+//
 // Work.  An *item* is one request's tile of query rows at one kv head; a row
 // is a (token, query head of the group) pair, token-major, so that the heads
 // that share a kv head share its loads.  An item's keys are cut into units of
-// kKeys keys, aligned in the sequence; its units are the tiles that hold a
-// sink followed by the tiles from the window's start to the last row.  All
+// kKeys keys, aligned in the sequence; its units are those that hold a sink
+// followed by those from the window's start to the last row.  All
 // units of all items, request by request and head by head, form one line that
 // is cut into equal shares, one a CTA, whatever the lengths: one long request
 // among short ones, or a batch of one, fills the machine.  A CTA whose share
@@ -19,6 +24,18 @@
 #include "paged.cuh"
 
 namespace cg {
+
+constexpr int kRowTile = 16;   // query rows of an item of the rows kernel (one matrix tile)
+constexpr int kRowKeys = 64;   // keys of a unit there
+
+// The line of work of one of the two kernels, in the workspace.
+struct Lane {
+  int64_t* cum;   // [slots + 1] units of one head before each slot
+  float* pieces;  // [2 * ctas][tile][dim] unnormalised outputs of cut items
+  float2* stats;  // [2 * ctas][tile] (maximum in log2 units, sum)
+  int ctas;       // CTAs of the kernel's grid, 0: not launched
+  int tile;       // query rows of an item
+};
 
 struct AttnParams {
   const uint16_t* q;
@@ -34,13 +51,13 @@ struct AttnParams {
   int window, sinks;
   int prefix_tokens, shared;
   float scale_log2;  // scale * log2(e)
-  // workspace
-  int64_t* row_cum;   // [slots + 1] units of a head before each slot of the rows kernel
-  float* row_pieces;  // [2 * row_ctas][kRowTile][dim]
-  float2* row_stats;  // [2 * row_ctas][kRowTile] (maximum in log2 units, sum)
-  float* whole;       // shared: [2][num_tokens][q_heads][dim], items that one CTA finished
+  uint32_t q_flip;    // sign bits of a negative scale, applied to q
+  int prefix_small;   // the rows of the whole batch fit the rows kernel
+  int tiled;          // requests above the rows kernel's size may be there (max_q)
+  Lane rows, tiles;
+  // shared: items that one CTA finished, [own, prefix][num_tokens][q_heads][dim]
+  float* whole;
   float2* whole_stats;
-  int row_ctas;
 };
 
 // What one request brings: its packed query rows and its keys.
@@ -98,6 +115,155 @@ __device__ __forceinline__ int unit_key(const Span& s, int u) {
   return (u < s.sink_units ? u : s.first_unit + u - s.sink_units) * kKeys;
 }
 
+struct Item {
+  Request req;
+  Span span;
+  int request;    // whose table, -1: the prefix's
+  int row, rows;  // first row of the tile among the request's rows, rows in it
+};
+
+// Slots of the kernels' lines.  Rows kernel: one a request.  Tile kernel:
+// request r's tiles start at slot floor(first row / kTile) + r, which leaves room
+// for every tile whatever the lengths; a slot without a tile costs nothing.
+// The prefix's tiles come last.
+template <int kTile>
+__device__ __forceinline__ int own_slots(const AttnParams& p) {
+  if (kTile == kRowTile) return p.num_requests;
+  return p.tiled ? int(int64_t(p.num_tokens) * p.group / kTile) + p.num_requests : 0;
+}
+
+template <int kTile>
+__device__ __forceinline__ int total_slots(const AttnParams& p) {
+  const bool prefix = p.shared && (p.prefix_small != 0) == (kTile == kRowTile);
+  return own_slots<kTile>(p) +
+         (prefix ? int((int64_t(p.num_tokens) * p.group + kTile - 1) / kTile) : 0);
+}
+
+template <int kTile>
+__device__ __forceinline__ int slot_base(const AttnParams& p, int r) {
+  if (kTile == kRowTile) return r;
+  int a = p.q_starts[r];
+  a = a < 0 ? 0 : (a > p.num_tokens ? p.num_tokens : a);
+  return int(int64_t(a) * p.group / kTile) + r;
+}
+
+// The item of slot x and its units for each kv head; 0 where it holds no rows.
+template <int kTile, int kKeys>
+__device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it) {
+  const int own = own_slots<kTile>(p);
+  if (x >= own) {
+    int n = p.q_starts[p.num_requests];
+    n = n < 0 ? 0 : (n > p.num_tokens ? p.num_tokens : n);
+    it.request = -1;
+    it.req.first = 0;
+    it.req.tokens = n;
+    it.req.keys = p.prefix_tokens;
+    it.req.row0 = p.prefix_tokens - 1;  // where a row sees all of the prefix
+    it.row = (x - own) * kTile;
+  } else {
+    int lo = x;
+    if (kTile != kRowTile) {
+      lo = 0;
+      int hi = p.num_requests - 1;  // the last request whose slots start at or before x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (slot_base<kTile>(p, mid) <= x) lo = mid;
+        else hi = mid - 1;
+      }
+    }
+    it.request = lo;
+    if (!load_request(p, lo, it.req)) {
+      report(p.status, CG_ERR_MISMATCH);
+      return 0;
+    }
+    if ((it.req.tokens * p.group <= kRowTile) != (kTile == kRowTile)) return 0;
+    it.row = kTile == kRowTile ? 0 : (x - slot_base<kTile>(p, lo)) * kTile;
+  }
+  const int rows = it.req.tokens * p.group;
+  if (it.row < 0 || it.row >= rows) return 0;
+  it.rows = rows - it.row < kTile ? rows - it.row : kTile;
+  if (it.request < 0) {
+    it.span = span_of<kKeys>(p.prefix_tokens - 1, p.prefix_tokens - 1, 0, 0);
+  } else {
+    const int t0 = div_of(it.row, p.group_div), t1 = div_of(it.row + it.rows - 1, p.group_div);
+    it.span = span_of<kKeys>(it.req.row0 + t0, it.req.row0 + t1, p.window, p.sinks);
+  }
+  // an item without a visible key still has its rows to write
+  return it.span.units > 0 ? it.span.units : 1;
+}
+
+// Position of a row of an item among its keys (at the last one for the prefix).
+__device__ __forceinline__ int row_position(const AttnParams& p, const Item& it, int row) {
+  return it.request < 0 ? it.req.row0 : it.req.row0 + div_of(row, p.group_div);
+}
+
+// CTAs that get a share: no share is empty.
+__device__ __forceinline__ int shares_of(const Lane& lane, int64_t units) {
+  return units < lane.ctas ? int(units) : lane.ctas;
+}
+
+// Row of the pool that holds a key, or -1 where the table has no such page.
+__device__ __forceinline__ int pool_row(const AttnParams& p, const int32_t* table, int key) {
+  const int col = div_of(key, p.page_div);
+  const int page = __ldg(table + col);
+  if (page < 0 || page >= p.num_pages) {
+    report(p.status, CG_ERR_MISMATCH);
+    return -1;
+  }
+  return page * p.page_tokens + (key - col * p.page_tokens);
+}
+
+// One CTA's share of a line, item by item.
+template <int kTile, int kKeys>
+struct Walk {
+  int64_t u, u_end, share0, cum;
+  int x, slots;
+  // the current part: units [first, last) of an item of `cost` units at `head`
+  Item it;
+  int head, first, last, piece;
+  bool whole;
+
+  __device__ __forceinline__ bool begin(const AttnParams& p, const Lane& lane) {
+    slots = total_slots<kTile>(p);
+    const int64_t units = lane.cum[slots] * p.kv_heads;
+    const int ctas = shares_of(lane, units);
+    if (int(blockIdx.x) >= ctas) return false;
+    u = units * blockIdx.x / ctas;
+    u_end = units * (blockIdx.x + 1) / ctas;
+    share0 = u;
+    x = 0;  // the last slot with kv_heads * cum[x] <= u
+    int hi = slots - 1;
+    while (x < hi) {
+      const int mid = (x + hi + 1) >> 1;
+      if (lane.cum[mid] * p.kv_heads <= u) x = mid;
+      else hi = mid - 1;
+    }
+    cum = lane.cum[x];
+    return true;
+  }
+
+  __device__ __forceinline__ bool next(const AttnParams& p) {
+    while (u < u_end && x < slots) {
+      const int cost = slot_item<kTile, kKeys>(p, x, it);
+      if (cost == 0 || u >= (cum + cost) * p.kv_heads) {
+        cum += cost;
+        ++x;
+        continue;
+      }
+      head = int((u - cum * p.kv_heads) / cost);
+      const int64_t item0 = cum * p.kv_heads + int64_t(head) * cost;
+      first = int(u - item0);
+      last = int((item0 + cost < u_end ? item0 + cost : u_end) - item0);
+      whole = first == 0 && last == cost;
+      piece = 2 * int(blockIdx.x) + (item0 >= share0 ? 1 : 0);
+      u = item0 + last;
+      if (it.span.units == 0) last = first;  // rows that see nothing
+      return true;
+    }
+    return false;
+  }
+};
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -110,10 +276,21 @@ __device__ __forceinline__ float weight_of(float m, float top) {
   return m == top ? (m == -__builtin_huge_valf() ? 0.f : 1.f) : exp2_fast(m - top);
 }
 
+constexpr float kNegInf = -__builtin_huge_valf();
+
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718056f;
+}
+
 // CTA that holds unit u when `units` are dealt to `ctas`: share c is
 // [c * units / ctas, (c + 1) * units / ctas).
 __device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas) {
   return int(((u + 1) * ctas - 1) / units);
 }
+
+// attend_tile.cu
+int tile_rows(int dim);  // query rows of an item of the tile kernel
+int tile_keys(int dim);
+cudaError_t launch_tiles(const AttnParams& p, bool bf16, cudaStream_t stream);
 
 }  // namespace cg

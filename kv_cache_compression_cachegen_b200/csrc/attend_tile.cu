@@ -1,0 +1,518 @@
+// attend_tile.cu -- attention over the paged pool as matrix products: chunks of
+// query rows, and a shared prefix under the rows of a whole batch.
+//
+// One CTA an SM, its roles by warp:
+//   warps 0-3, 4-7   softmax of query tile 0 and 1 (128 rows each, a row a
+//                    thread): scores out of tensor memory, running maximum and
+//                    sum, weights back into tensor memory; output of the item
+//   warps 8-11       K and V rows from the pages to shared memory (cp.async in
+//                    the 128-byte swizzle; a page may end anywhere in a tile)
+//   warp 12          one thread issues the products:
+//                      S = Q K^T   both operands in shared memory
+//                      O += P V    P in tensor memory, V along its channels
+// The two query tiles take turns: while one's scores are in softmax the tensor
+// cores work on the other's products.  The weights P overwrite their scores.
+//
+// The running maximum m moves only when a score passes it by 2^8: until then
+// weights up to 2^8 are in range of fp16 and bf16 alike, nothing is lost, and
+// the output need not be read back from tensor memory to be rescaled.
+#include <algorithm>
+
+#include "attend.cuh"
+#include "tcgen05.cuh"
+
+namespace cg {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
+
+template <int DC>
+struct Geometry {
+  static constexpr int kTiles = DC <= 2 ? 2 : 1;      // query tiles of 128 rows
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kKeys = DC <= 2 ? 128 : 64;    // keys of a unit
+  static constexpr int kStages = 4;                   // K and V tiles in flight
+  static constexpr int kQBytes = 128 * 128;           // a 64-channel block of a query tile
+  static constexpr int kBlock = kKeys * 128;          // a 64-channel block of a K or V tile
+  static constexpr int kStage = DC * kBlock;
+  static constexpr int kSmem = kTiles * DC * kQBytes + kStages * kStage + 1024;
+  // tensor memory columns: scores, then outputs
+  static constexpr uint32_t kS = 0, kSStep = 128;
+  static constexpr uint32_t kO = 256, kOStep = 128;
+};
+
+struct Bars {
+  uint32_t full, empty, q_full, s_full, p_full, o_full;  // each the first of its array
+};
+
+// A row that met a value which is not finite, computed again by a warp from
+// the definition: a masked key's weight of zero does not hide an infinity or a
+// NaN in the matrix product.  o: four channels a lane and 128 channels apart.
+template <typename T>
+__device__ __forceinline__ void recompute_row(const AttnParams& p, const Item& it, int head, int row, int kKeys,
+                              int first, int last, float (&o)[2][4], float& m, float& l) {
+  const int lane = threadIdx.x & 31;
+  const bool prefix = it.request < 0;
+  const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
+  const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
+  const int tok = div_of(row, p.group_div), at = row_position(p, it, row);
+  const uint16_t* q = p.q + int64_t(it.req.first + tok) * p.q_stride +
+                      int64_t(head * p.group + row - tok * p.group) * p.dim;
+  const int64_t step = int64_t(p.kv_heads) * p.dim;
+  m = kNegInf;
+  l = 0.f;
+  for (int h = 0; h < 2; ++h)
+    for (int e = 0; e < 4; ++e) o[h][e] = 0.f;
+  for (int u = first; u < last; ++u) {
+    const int unit = u < it.span.sink_units ? u : it.span.first_unit + u - it.span.sink_units;
+    for (int k0 = 0; k0 < kKeys; k0 += 32) {
+      const int key = unit * kKeys + k0 + lane;
+      int from = -1;
+      if (sees(key, at, window, sinks)) from = pool_row(p, table, key);
+      float s = kNegInf;
+      if (from >= 0) {
+        const uint16_t* k = p.k_pool + from * step + int64_t(head) * p.dim;
+        float dot = 0.f;
+        for (int d = 0; d < p.dim; d += 2) {
+          const float2 a = T::unpack(*reinterpret_cast<const uint32_t*>(q + d) ^ p.q_flip);
+          const float2 b = T::unpack(*reinterpret_cast<const uint32_t*>(k + d));
+          dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
+        }
+        s = dot * p.scale_log2;
+      }
+      float top = s;
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+      top = fmaxf(top, m);
+      const float f = weight_of(m, top);
+      m = top;
+      l *= f;
+      for (int h = 0; h < 2; ++h)
+        for (int e = 0; e < 4; ++e) o[h][e] *= f;
+      const float w = s == kNegInf ? 0.f : exp2_fast(s - m);
+      for (int j = 0; j < 32; ++j) {
+        const int src = __shfl_sync(~0u, from, j);
+        const float wj = __shfl_sync(~0u, w, j);
+        if (src < 0) continue;
+        l += wj;
+        const uint16_t* v = p.v_pool + src * step + int64_t(head) * p.dim;
+        for (int h = 0; h < 2; ++h)
+          if (128 * h + 4 * lane < p.dim) {
+            const uint2 x = *reinterpret_cast<const uint2*>(v + 128 * h + 4 * lane);
+            const float2 a = T::unpack(x.x), b = T::unpack(x.y);
+            o[h][0] = fmaf(wj, a.x, o[h][0]);
+            o[h][1] = fmaf(wj, a.y, o[h][1]);
+            o[h][2] = fmaf(wj, b.x, o[h][2]);
+            o[h][3] = fmaf(wj, b.y, o[h][3]);
+          }
+      }
+    }
+  }
+}
+
+template <typename T, int DC>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
+  using G = Geometry<DC>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars_mem[2 * G::kStages + 8];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int dead_mem;
+  __shared__ uint32_t no_page[4][4];  // keys of a unit whose page is not in the pool
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t q_smem = base;
+  const uint32_t kv_smem = base + G::kTiles * DC * G::kQBytes;
+  volatile int* dead = &dead_mem;
+  Bars bar;
+  bar.full = smem_addr(bars_mem);
+  bar.empty = bar.full + 8 * G::kStages;
+  bar.q_full = bar.empty + 8 * G::kStages;
+  bar.s_full = bar.q_full + 16;
+  bar.p_full = bar.s_full + 16;
+  bar.o_full = bar.p_full + 16;
+
+  if (threadIdx.x == 0) {
+    dead_mem = 0;
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(bar.full + 8 * i, 4);
+      mbar_init(bar.empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar.q_full + 8 * i, 4);
+      mbar_init(bar.s_full + 8 * i, 1);
+      mbar_init(bar.p_full + 8 * i, 4);
+      mbar_init(bar.o_full + 8 * i, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) tmem_alloc(smem_addr(&tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  Walk<G::kRows, G::kKeys> w;
+  const bool any = w.begin(p, p.tiles);
+  const int D = p.dim;
+
+  // Registers: 512 threads start with 128 each, 65,536 in all; the softmax warps
+  // hold a row of scores each and take 2 * 128 * 192, the others 2 * 128 * 64.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int tile = warp >> 2;
+    const int r = threadIdx.x & 127;  // row in the tile, lane of tensor memory
+    const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tmem + lanes + G::kS + tile * G::kSStep;
+    const uint32_t t_o = tmem + lanes + G::kO + tile * G::kOStep;
+    uint32_t s_phase = 0, o_phase = 0, unit_count = 0;
+    bool ok = any && tile < G::kTiles;
+    while (ok && w.next(p)) {
+      const Item& it = w.it;
+      const uint32_t before = unit_count;
+      unit_count += w.last - w.first;
+      if (it.rows <= 128 * tile) continue;  // no rows in this tile
+      const bool real = 128 * tile + r < it.rows;
+      const int row = it.row + (real ? 128 * tile + r : it.rows - 1);
+      const int tok = div_of(row, p.group_div);
+      const int64_t t = it.req.first + tok;
+      const int qh = w.head * p.group + row - tok * p.group;
+      const bool prefix = it.request < 0;
+      const int pos = row_position(p, it, row);
+      const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
+      float m = kNegInf, l = 0.f;
+      bool mixed = false;  // some unit had keys that a row does not see
+      if (w.first < w.last) {
+        // Q: eight lanes a row, so that a row's bytes are read together
+        for (int i = 0; i < 32; i += 4) {
+          const int rr = 32 * (warp & 3) + i + (lane >> 3);
+          const bool have = 128 * tile + rr < it.rows;
+          const int qrow = it.row + 128 * tile + rr;
+          const int qtok = div_of(qrow, p.group_div);
+          const uint16_t* src = p.q + int64_t(it.req.first + qtok) * p.q_stride +
+                                int64_t(w.head * p.group + qrow - qtok * p.group) * D;
+#pragma unroll
+          for (int b = 0; b < DC; ++b) {
+            const int c = lane & 7;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (have && 64 * b + 8 * c < D)
+              v = *reinterpret_cast<const uint4*>(src + 64 * b + 8 * c);
+            v.x ^= p.q_flip, v.y ^= p.q_flip, v.z ^= p.q_flip, v.w ^= p.q_flip;
+            const uint32_t dst = q_smem + (tile * DC + b) * G::kQBytes + rr * 128 +
+                                 ((c ^ (rr & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y),
+                         "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.q_full + 8 * tile);
+      }
+      for (int u = w.first; u < w.last; ++u) {
+        if (!(ok = mbar_wait(bar.s_full + 8 * tile, s_phase, dead))) break;
+        s_phase ^= 1;
+        tc_fence_after();
+        uint32_t raw[G::kKeys];
+#pragma unroll
+        for (int j = 0; j < G::kKeys; j += 64) tmem_load64(t_s + j, raw + j);
+        const int key0 = unit_key<G::kKeys>(it.span, u);
+        // the whole unit is seen by the row, or its keys are looked at one by one
+        const int end = key0 + G::kKeys - 1;
+        const uint32_t* hole = no_page[(before + u - w.first) & 3];
+        uint32_t holes = 0;
+#pragma unroll
+        for (int i = 0; i < G::kKeys / 32; ++i) holes |= hole[i];
+        const bool full = end <= pos && (window == 0 || pos - key0 < window || end < sinks);
+        if (!__all_sync(~0u, full && holes == 0)) {
+          mixed = true;
+#pragma unroll
+          for (int j = 0; j < G::kKeys; ++j) {
+            const bool see = sees(key0 + j, pos, window, sinks) && !((hole[j / 32] >> (j & 31)) & 1);
+            if (!see) raw[j] = __float_as_uint(kNegInf);
+          }
+        }
+        float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+        for (int j = 0; j < G::kKeys; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(raw[j]));
+        const float most =
+            fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+        const bool move = most > m + kSlack || (m == kNegInf && most > kNegInf);
+        if (__any_sync(~0u, move)) {
+          const float next = move ? most : m;
+          const float f = m == next ? 1.f : exp2_fast(m - next);
+          m = next;
+          l *= f;
+          if (u > w.first) {
+            // the products into O so far are done: S came after them
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_load16(t_o + c, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_store16(t_o + c, o);
+            }
+          }
+        }
+        const float shift = m == kNegInf ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < G::kKeys; j += 2) {
+          const float a = exp2_fast(fmaf(__uint_as_float(raw[j]), p.scale_log2, shift));
+          const float b = exp2_fast(fmaf(__uint_as_float(raw[j + 1]), p.scale_log2, shift));
+          sum[(j >> 1) & 1] += a;
+          sum[2 + ((j >> 1) & 1)] += b;
+          // rounded to the pool's type for the product with V: half a step of it
+          // relative to each weight; the sum is not
+          raw[j / 2] = T::pack(a, b);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+        for (int j = 0; j < G::kKeys / 2; j += 32) tmem_store32(t_s + j, raw + j);
+        tmem_store_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.p_full + 8 * tile);
+      }
+      if (!ok) break;
+      // ---- the rows' output
+      const bool none = w.first >= w.last;
+      if (!none) {
+        if (!(ok = mbar_wait(bar.o_full + 8 * tile, o_phase, dead))) break;
+        o_phase ^= 1;
+        tc_fence_after();
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t piece = int64_t(w.piece) * G::kRows + 128 * tile + r;
+      const int64_t whole = (int64_t(prefix) * p.num_tokens + t) * p.q_heads + qh;
+      float* part = !w.whole ? p.tiles.pieces + piece * D : p.whole + whole * D;
+      const bool direct = w.whole && !p.shared;
+      uint16_t* out = p.out + t * p.out_stride + int64_t(qh) * D;
+      bool odd = !(l - l == 0.f);
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        if (none) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = 0;
+        } else {
+          tmem_load16(t_o + c, o);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float v = __uint_as_float(o[j]);
+          odd |= !(v - v == 0.f);
+        }
+        if (real && direct) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 8) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = T::pack(__uint_as_float(o[j + 2 * e]) * inv,
+                             __uint_as_float(o[j + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(out + c + j) = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        } else if (real) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<uint4*>(part + c + j) =
+                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        }
+        __syncwarp();
+      }
+      if (real) {
+        if (!direct) (w.whole ? p.whole_stats[whole] : p.tiles.stats[piece]) = make_float2(m, l);
+        else if (p.lse != nullptr) p.lse[t * p.q_heads + qh] = log_sum(m, l);
+      }
+      // rows whose sums are not finite, where some keys were hidden
+      uint32_t again = __ballot_sync(~0u, real && mixed && odd);
+      __syncwarp();
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const int rr = 128 * tile + 32 * (warp & 3) + src;
+        float o[2][4], mm, ll;
+        recompute_row<T>(p, it, w.head, it.row + rr, G::kKeys, w.first, w.last, o, mm, ll);
+        const float scale = direct ? (ll == 0.f ? 0.f : 1.f / ll) : 1.f;
+        const int64_t t2 = __shfl_sync(~0u, t, src);
+        const int qh2 = __shfl_sync(~0u, qh, src);
+        const int64_t whole2 = __shfl_sync(~0u, whole, src), piece2 = __shfl_sync(~0u, piece, src);
+        for (int h = 0; h < 2; ++h) {
+          const int d = 128 * h + 4 * lane;
+          if (d >= D) continue;
+          if (direct)
+            *reinterpret_cast<uint2*>(p.out + t2 * p.out_stride + int64_t(qh2) * D + d) = make_uint2(
+                T::pack(o[h][0] * scale, o[h][1] * scale), T::pack(o[h][2] * scale, o[h][3] * scale));
+          else
+            *reinterpret_cast<float4*>((w.whole ? p.whole + whole2 * D : p.tiles.pieces + piece2 * D) +
+                                       d) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
+        }
+        if (lane == 0) {
+          if (!direct) (w.whole ? p.whole_stats[whole2] : p.tiles.stats[piece2]) = make_float2(mm, ll);
+          else if (p.lse != nullptr) p.lse[t2 * p.q_heads + qh2] = log_sum(mm, ll);
+        }
+      }
+      tc_fence_before();
+    }
+    if (!ok && any && tile < G::kTiles && lane == 0) report(p.status, CG_ERR_CUDA);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp < 12) {
+      // ---- K and V to shared memory
+      const int wk = warp - 8;
+      constexpr int kLanes = 8 * DC;            // lanes of a row (16 bytes each)
+      constexpr int kPer = 32 / kLanes;         // rows a warp copies at a time
+      constexpr int kMine = G::kKeys / 4;       // rows of a tile that are this warp's
+      const int c = lane % kLanes, sub = lane / kLanes;
+      const int64_t step = int64_t(p.kv_heads) * D;
+      uint32_t stage = 0, phase = 1, tiles = 0, unit_count = 0;
+      bool ok = any;
+      while (ok && w.next(p)) {
+        const Item& it = w.it;
+        const bool prefix = it.request < 0;
+        const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
+        const int64_t col = int64_t(w.head) * D + 8 * c;
+        for (int u = w.first; ok && u < w.last; ++u, ++unit_count) {
+          // lane i knows the pool row of the warp's i-th key; -1: no row of the item sees it
+          int mine = -1;
+          bool hole = false;
+          if (lane < kMine) {
+            const int key = unit_key<G::kKeys>(it.span, u) + kMine * wk + lane;
+            if (key < it.span.hi && (key >= it.span.lo || key < it.span.sink_end)) {
+              mine = pool_row(p, table, key);
+              hole = mine < 0;
+            }
+          }
+          const uint32_t holes = __ballot_sync(~0u, hole);
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!(ok = mbar_wait(bar.empty + 8 * stage, phase, dead))) break;
+            if (kv == 0 && lane == 0) {
+              if constexpr (kMine == 32) no_page[unit_count & 3][wk] = holes;
+              else reinterpret_cast<uint16_t*>(no_page[unit_count & 3])[wk] = uint16_t(holes);
+            }
+            const uint16_t* pool = (kv ? p.v_pool : p.k_pool) + col;
+            const uint32_t dst = kv_smem + stage * G::kStage + (c >> 3) * G::kBlock;
+#pragma unroll 4
+            for (int i = 0; i < kMine; i += kPer) {
+              const int src = __shfl_sync(~0u, mine, i + sub);
+              const int key = kMine * wk + i + sub;
+              if (8 * c < D)
+                cp_async16(dst + key * 128 + (((c & 7) ^ (key & 7)) << 4),
+                           src >= 0 ? pool + src * step : pool, src >= 0 ? 16 : 0);
+            }
+            cp_async_commit();
+            // the tile before this one has landed: pass it on
+            if (tiles > 0) {
+              cp_async_wait<1>();
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar.full + 8 * ((stage + G::kStages - 1) % G::kStages));
+            }
+            ++tiles;
+            if (++stage == G::kStages) stage = 0, phase ^= 1;
+          }
+        }
+      }
+      cp_async_wait<0>();
+      if (tiles > 0) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.full + 8 * ((stage + G::kStages - 1) % G::kStages));
+      }
+    } else if (warp == 12 && lane == 0) {
+      // ---- the products
+      constexpr bool kBf16 = T::kBf16;
+      const uint32_t qk = mma_desc(kBf16, false, 128, G::kKeys);
+      const uint32_t pv = mma_desc(kBf16, true, 128, D);
+      uint32_t stage = 0, phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      bool ok = any;
+      const auto step = [&]() {
+        if (++stage == G::kStages) stage = 0, phase ^= 1;
+      };
+      const auto scores = [&](int tile, uint32_t k_smem) {
+#pragma unroll 1
+        for (int k = 0; k < D; k += 16) {
+          const uint32_t in = (k >> 6), off = (k & 63) * 2;
+          mma_ss(tmem + G::kS + tile * G::kSStep,
+                 smem_desc(q_smem + (tile * DC + in) * G::kQBytes + off, 16, 1024),
+                 smem_desc(k_smem + in * G::kBlock + off, 16, 1024), qk, k > 0);
+        }
+        mma_commit(bar.s_full + 8 * tile);
+      };
+      while (ok && w.next(p)) {
+        const int active = w.it.rows > 128 ? 2 : 1;
+        if (w.first >= w.last) continue;
+        if (!(ok = mbar_wait(bar.full + 8 * stage, phase, dead))) break;
+        uint32_t k_stage = stage;
+        step();
+        for (int tile = 0; tile < active; ++tile) {
+          if (!(ok = mbar_wait(bar.q_full + 8 * tile, q_phase[tile], dead))) break;
+          q_phase[tile] ^= 1;
+          tc_fence_after();
+          scores(tile, kv_smem + k_stage * G::kStage);
+        }
+        if (!ok) break;
+        mma_commit(bar.empty + 8 * k_stage);
+        for (int u = w.first; ok && u < w.last; ++u) {
+          const bool more = u + 1 < w.last;
+          if (!(ok = mbar_wait(bar.full + 8 * stage, phase, dead))) break;
+          const uint32_t v_stage = stage;
+          step();
+          if (more) {
+            if (!(ok = mbar_wait(bar.full + 8 * stage, phase, dead))) break;
+            k_stage = stage;
+            step();
+          }
+          for (int tile = 0; tile < active; ++tile) {
+            if (!(ok = mbar_wait(bar.p_full + 8 * tile, p_phase[tile], dead))) break;
+            p_phase[tile] ^= 1;
+            tc_fence_after();
+            const uint32_t v_smem = kv_smem + v_stage * G::kStage;
+#pragma unroll 1
+            for (int k = 0; k < G::kKeys; k += 16)
+              mma_ts(tmem + G::kO + tile * G::kOStep, tmem + G::kS + tile * G::kSStep + k / 2,
+                     smem_desc(v_smem + k * 128, G::kBlock, 1024), pv, u > w.first || k > 0);
+            if (more) scores(tile, kv_smem + k_stage * G::kStage);
+            else mma_commit(bar.o_full + 8 * tile);
+          }
+          if (!ok) break;
+          mma_commit(bar.empty + 8 * v_stage);
+          if (more) mma_commit(bar.empty + 8 * k_stage);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+template <typename T, int DC>
+cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
+  const cudaError_t err = cudaFuncSetAttribute(
+      tile_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geometry<DC>::kSmem);
+  if (err != cudaSuccess) return err;
+  tile_kernel<T, DC><<<p.tiles.ctas, kThreads, Geometry<DC>::kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const AttnParams& p, cudaStream_t stream) {
+  if (p.dim <= 64) return launch<T, 1>(p, stream);
+  if (p.dim <= 128) return launch<T, 2>(p, stream);
+  return launch<T, 4>(p, stream);
+}
+
+}  // namespace
+
+int tile_rows(int dim) { return dim <= 128 ? Geometry<2>::kRows : Geometry<4>::kRows; }
+int tile_keys(int dim) { return dim <= 128 ? Geometry<2>::kKeys : Geometry<4>::kKeys; }
+
+cudaError_t launch_tiles(const AttnParams& p, bool bf16, cudaStream_t stream) {
+  return bf16 ? launch_type<BF16>(p, stream) : launch_type<F16>(p, stream);
+}
+
+}  // namespace cg

@@ -38,6 +38,7 @@ __device__ __forceinline__ void report(int32_t* status, int32_t code) {
 
 // Type of a pool: fp16 or bf16 values, moved as 32-bit pairs.
 struct F16 {
+  static constexpr bool kBf16 = false;
   __device__ static __forceinline__ float2 unpack(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
   }
@@ -61,6 +62,7 @@ struct F16 {
 };
 
 struct BF16 {
+  static constexpr bool kBf16 = true;
   __device__ static __forceinline__ float2 unpack(uint32_t v) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
   }
