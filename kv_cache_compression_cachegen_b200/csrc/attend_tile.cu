@@ -5,17 +5,22 @@
 //   warps 0-3, 4-7   softmax of query tile 0 and 1 (128 rows each, a row a
 //                    thread): scores out of tensor memory, running maximum and
 //                    sum, weights back into tensor memory; output of the item
-//   warps 8-11       K and V rows from the pages to shared memory (cp.async in
-//                    the 128-byte swizzle; a page may end anywhere in a tile)
-//   warp 12          one thread issues the products:
+//   warps 10, 11     K and V from the pages to shared memory, in the 128-byte
+//                    swizzle: by TMA where all of a warp's half of a tile can be
+//                    seen and lies in runs of eight rows or more, else row by row
+//                    (cp.async; a page may end anywhere in a tile) with zeros for
+//                    what no row of the item sees
+//   warp 8           one thread issues the products:
 //                      S = Q K^T   both operands in shared memory
 //                      O += P V    P in tensor memory, V along its channels
 // The two query tiles take turns: while one's scores are in softmax the tensor
-// cores work on the other's products.  The weights P overwrite their scores.
+// cores work on the other's products.
 //
 // The running maximum m moves only when a score passes it by 2^8: until then
 // weights up to 2^8 are in range of fp16 and bf16 alike, nothing is lost, and
 // the output need not be read back from tensor memory to be rescaled.
+#include <cuda.h>  // tensor-map types only; the encoder is looked up at run time
+
 #include <algorithm>
 
 #include "attend.cuh"
@@ -24,7 +29,8 @@
 namespace cg {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;  // 168 registers a thread: a softmax thread holds 128 scores
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoadWarps = 2;
 constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
 
 template <int DC>
@@ -37,14 +43,50 @@ struct Geometry {
   static constexpr int kBlock = kKeys * 128;          // a 64-channel block of a K or V tile
   static constexpr int kStage = DC * kBlock;
   static constexpr int kSmem = kTiles * DC * kQBytes + kStages * kStage + 1024;
-  // tensor memory columns: scores, then outputs
+  // Tensor memory columns of scores, weights and outputs (of tile 1: kStep on).
+  // Products are only sure to follow one another in order where their shapes
+  // are alike, so the next scores may overwrite weights that a product still
+  // reads only there: with 65 to 128 channels, where there is no room for both,
+  // both products are made 128 x 128 (columns behind the channels are not
+  // read).  Elsewhere the weights have columns of their own.
   static constexpr uint32_t kS = 0, kSStep = 128;
-  static constexpr uint32_t kO = 256, kOStep = 128;
+  static constexpr uint32_t kP = DC == 1 ? 256 : (DC == 2 ? 0 : 64);
+  static constexpr uint32_t kPStep = DC == 1 ? 64 : 128;
+  static constexpr uint32_t kO = DC == 1 ? 384 : 256;
+  static constexpr uint32_t kOStep = DC == 1 ? 64 : 128;
 };
 
 struct Bars {
   uint32_t full, empty, q_full, s_full, p_full, o_full;  // each the first of its array
 };
+
+// 2^x of two values without the special-function unit, which alone would take
+// as long over a unit's weights as the tensor cores over its products: n =
+// round(x) by adding 1.5 * 2^23, a polynomial for 2^(x - n) on [-1/2, 1/2], n
+// added to the exponent.  The coefficients are the minimax ones of degree 5 for
+// the relative error (Remez exchange), 2^-23.7, and 2^-22 as evaluated in fp32
+// -- what ex2.approx has.  Below -125 the result stays 2^-125.
+__device__ __forceinline__ float2 exp2_pair(float2 x) {
+  const float2 magic = make_float2(12582912.f, 12582912.f);
+  const float2 minus = make_float2(-12582912.f, -12582912.f);
+  x = make_float2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  const float2 t = add_pair(x, magic);
+  const float2 n = add_pair(t, minus);
+  const float2 r = fma_pair(n, make_float2(-1.f, -1.f), x);
+  float2 y = make_float2(0.0013276472f, 0.0013276472f);
+  y = fma_pair(y, r, make_float2(0.009675541f, 0.009675541f));
+  y = fma_pair(y, r, make_float2(0.05550713f, 0.05550713f));
+  y = fma_pair(y, r, make_float2(0.2402212f, 0.2402212f));
+  y = fma_pair(y, r, make_float2(0.69314694f, 0.69314694f));
+  y = fma_pair(y, r, make_float2(1.0000001f, 1.0000001f));
+  return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// The lowest n bits.
+__device__ __forceinline__ uint32_t below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+}
 
 // A row that met a value which is not finite, computed again by a warp from
 // the definition: a masked key's weight of zero does not hide an infinity or a
@@ -111,7 +153,9 @@ __device__ __forceinline__ void recompute_row(const AttnParams& p, const Item& i
 }
 
 template <typename T, int DC>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(AttnParams p, const __grid_constant__ CUtensorMap k_map,
+                const __grid_constant__ CUtensorMap v_map, int box) {
   using G = Geometry<DC>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars_mem[2 * G::kStages + 8];
@@ -134,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
   if (threadIdx.x == 0) {
     dead_mem = 0;
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(bar.full + 8 * i, 4);
+      mbar_init(bar.full + 8 * i, kLoadWarps);
       mbar_init(bar.empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -145,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) tmem_alloc(smem_addr(&tmem_slot), 512);
+  if (warp == kMmaWarp) tmem_alloc(smem_addr(&tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -155,14 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
   const bool any = w.begin(p, p.tiles);
   const int D = p.dim;
 
-  // Registers: 512 threads start with 128 each, 65,536 in all; the softmax warps
-  // hold a row of scores each and take 2 * 128 * 192, the others 2 * 128 * 64.
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int tile = warp >> 2;
     const int r = threadIdx.x & 127;  // row in the tile, lane of tensor memory
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t t_s = tmem + lanes + G::kS + tile * G::kSStep;
+    const uint32_t t_p = tmem + lanes + G::kP + tile * G::kPStep;
     const uint32_t t_o = tmem + lanes + G::kO + tile * G::kOStep;
     uint32_t s_phase = 0, o_phase = 0, unit_count = 0;
     bool ok = any && tile < G::kTiles;
@@ -216,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
 #pragma unroll
         for (int j = 0; j < G::kKeys; j += 64) tmem_load64(t_s + j, raw + j);
         const int key0 = unit_key<G::kKeys>(it.span, u);
-        // the whole unit is seen by the row, or its keys are looked at one by one
+        // the whole unit is seen by the row, or its keys are hidden one by one
         const int end = key0 + G::kKeys - 1;
         const uint32_t* hole = no_page[(before + u - w.first) & 3];
         uint32_t holes = 0;
@@ -225,10 +267,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
         const bool full = end <= pos && (window == 0 || pos - key0 < window || end < sinks);
         if (!__all_sync(~0u, full && holes == 0)) {
           mixed = true;
+          // keys before `past` are behind the window
+          const int past = window == 0 ? 0 : int(max(0ll, (long long)pos - window + 1));
 #pragma unroll
-          for (int j = 0; j < G::kKeys; ++j) {
-            const bool see = sees(key0 + j, pos, window, sinks) && !((hole[j / 32] >> (j & 31)) & 1);
-            if (!see) raw[j] = __float_as_uint(kNegInf);
+          for (int i = 0; i < G::kKeys / 32; ++i) {
+            const int from = key0 + 32 * i;
+            const uint32_t seen =
+                below(pos + 1 - from) & (~below(past - from) | below(sinks - from)) & ~hole[i];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((seen >> j) & 1)) raw[32 * i + j] = __float_as_uint(kNegInf);
           }
         }
         float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
@@ -254,20 +302,27 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
           }
         }
         const float shift = m == kNegInf ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+        const float2 shift2 = make_float2(shift, shift);
 #pragma unroll
         for (int j = 0; j < G::kKeys; j += 2) {
-          const float a = exp2_fast(fmaf(__uint_as_float(raw[j]), p.scale_log2, shift));
-          const float b = exp2_fast(fmaf(__uint_as_float(raw[j + 1]), p.scale_log2, shift));
-          sum[(j >> 1) & 1] += a;
-          sum[2 + ((j >> 1) & 1)] += b;
+          const float2 x = fma_pair(
+              make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])), scale2, shift2);
+          // three of eight on the multiply-add pipe: see exp2_pair
+          const int turn = (j >> 1) & 7;
+          const float2 e = turn == 1 || turn == 4 || turn == 6
+                               ? exp2_pair(x)
+                               : make_float2(exp2_fast(x.x), exp2_fast(x.y));
+          sum[(j >> 1) & 1] = add_pair(sum[(j >> 1) & 1], e);
           // rounded to the pool's type for the product with V: half a step of it
           // relative to each weight; the sum is not
-          raw[j / 2] = T::pack(a, b);
+          raw[j / 2] = T::pack(e.x, e.y);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // nothing seen so far: exp2_pair leaves 2^-125 where the weight is zero
+        l = m == kNegInf ? 0.f : l + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
 #pragma unroll
-        for (int j = 0; j < G::kKeys / 2; j += 32) tmem_store32(t_s + j, raw + j);
+        for (int j = 0; j < G::kKeys / 2; j += 32) tmem_store32(t_p + j, raw + j);
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
@@ -355,88 +410,156 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
     }
     if (!ok && any && tile < G::kTiles && lane == 0) report(p.status, CG_ERR_CUDA);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp < 12) {
+    if (warp >= kLoadWarp) {
       // ---- K and V to shared memory
-      const int wk = warp - 8;
+      const int wk = warp - kLoadWarp;
       constexpr int kLanes = 8 * DC;            // lanes of a row (16 bytes each)
       constexpr int kPer = 32 / kLanes;         // rows a warp copies at a time
-      constexpr int kMine = G::kKeys / 4;       // rows of a tile that are this warp's
+      constexpr int kMine = G::kKeys / kLoadWarps;  // rows of a tile that are this warp's
+      constexpr int kOwn = kMine / 32;              // of these, a lane's
       const int c = lane % kLanes, sub = lane / kLanes;
       const int64_t step = int64_t(p.kv_heads) * D;
       uint32_t stage = 0, phase = 1, tiles = 0, unit_count = 0;
+      uint32_t copied = 0;  // the latest tiles, a bit each: this warp's half came by cp.async
       bool ok = any;
+      // Halves that came by cp.async are passed on kLag tiles behind the one that
+      // is being asked for, when they have landed, so that more are on their way.
+      constexpr int kLag = 2;
+      const auto pass_on = [&](uint32_t behind) {
+        if ((copied >> (behind - 1)) & 1) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0)
+            mbar_arrive(bar.full + 8 * ((stage + G::kStages - behind) % G::kStages));
+        }
+      };
+      const int boxes = box > 0 ? kMine / box * DC : 0;  // TMA boxes of the warp's half of a tile
       while (ok && w.next(p)) {
         const Item& it = w.it;
         const bool prefix = it.request < 0;
         const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
         const int64_t col = int64_t(w.head) * D + 8 * c;
-        for (int u = w.first; ok && u < w.last; ++u, ++unit_count) {
-          // lane i knows the pool row of the warp's i-th key; -1: no row of the item sees it
-          int mine = -1;
-          bool hole = false;
-          if (lane < kMine) {
-            const int key = unit_key<G::kKeys>(it.span, u) + kMine * wk + lane;
-            if (key < it.span.hi && (key >= it.span.lo || key < it.span.sink_end)) {
-              mine = pool_row(p, table, key);
-              hole = mine < 0;
+        // Lane i has the warp's keys i, i + 32, ... of the unit; their pages are
+        // looked up a unit ahead.  -2: no row of the item sees the key.
+        int key_ahead[kOwn], page_ahead[kOwn], mine[kOwn];
+        const auto look_up = [&](int u) {
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) {
+            page_ahead[i] = -2;
+            key_ahead[i] = 0;
+            if (u < w.last) {
+              const int key = unit_key<G::kKeys>(it.span, u) + kMine * wk + 32 * i + lane;
+              if (key < it.span.hi && (key >= it.span.lo || key < it.span.sink_end))
+                page_ahead[i] = max(-1, __ldg(table + div_of(key, p.page_div)));
+              key_ahead[i] = key;
             }
           }
-          const uint32_t holes = __ballot_sync(~0u, hole);
+        };
+        look_up(w.first);
+        for (int u = w.first; ok && u < w.last; ++u, ++unit_count) {
+          uint32_t holes[kOwn];
+          bool there = box > 0;  // every key of the warp's half can be read
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) {
+            const bool hole = page_ahead[i] == -1 || page_ahead[i] >= p.num_pages;
+            mine[i] = -1;
+            if (page_ahead[i] >= 0 && !hole)
+              mine[i] = page_ahead[i] * p.page_tokens +
+                        (key_ahead[i] - div_of(key_ahead[i], p.page_div) * p.page_tokens);
+            holes[i] = __ballot_sync(~0u, hole);
+            there = there && mine[i] >= 0;
+            if (holes[i] != 0 && lane == 0) report(p.status, CG_ERR_MISMATCH);
+          }
+          there = __all_sync(~0u, there);
+          look_up(u + 1);
           for (int kv = 0; kv < 2; ++kv) {
             if (!(ok = mbar_wait(bar.empty + 8 * stage, phase, dead))) break;
             if (kv == 0 && lane == 0) {
-              if constexpr (kMine == 32) no_page[unit_count & 3][wk] = holes;
-              else reinterpret_cast<uint16_t*>(no_page[unit_count & 3])[wk] = uint16_t(holes);
+#pragma unroll
+              for (int i = 0; i < kOwn; ++i) no_page[unit_count & 3][wk * kOwn + i] = holes[i];
             }
-            const uint16_t* pool = (kv ? p.v_pool : p.k_pool) + col;
-            const uint32_t dst = kv_smem + stage * G::kStage + (c >> 3) * G::kBlock;
-#pragma unroll 4
-            for (int i = 0; i < kMine; i += kPer) {
-              const int src = __shfl_sync(~0u, mine, i + sub);
-              const int key = kMine * wk + i + sub;
-              if (8 * c < D)
-                cp_async16(dst + key * 128 + (((c & 7) ^ (key & 7)) << 4),
-                           src >= 0 ? pool + src * step : pool, src >= 0 ? 16 : 0);
+            __syncwarp();
+            const uint32_t tile_smem = kv_smem + stage * G::kStage;
+            if (there) {
+              // whole boxes of keys that follow one another in a page
+              if (lane == 0) mbar_expect(bar.full + 8 * stage, kMine * 128 * DC);
+              __syncwarp();
+              for (int i0 = 0; i0 < boxes; i0 += 32) {
+                const int i = i0 + lane, b = i % DC, key = i / DC * box;
+                int row = __shfl_sync(~0u, mine[0], key & 31);
+                if constexpr (kOwn == 2) {
+                  const int upper = __shfl_sync(~0u, mine[kOwn - 1], key & 31);
+                  if (key >= 32) row = upper;
+                }
+                if (i < boxes)
+                  tma_load3(tile_smem + b * G::kBlock + (kMine * wk + key) * 128,
+                            kv ? &v_map : &k_map, 64 * b, w.head, row, bar.full + 8 * stage);
+              }
+            } else {
+              const uint16_t* pool = (kv ? p.v_pool : p.k_pool) + col;
+              const uint32_t dst = tile_smem + (c >> 3) * G::kBlock;
+#pragma unroll
+              for (int o = 0; o < kOwn; ++o)
+#pragma unroll 8
+                for (int i = 0; i < 32; i += kPer) {
+                  const int src = __shfl_sync(~0u, mine[o], i + sub);
+                  const int key = kMine * wk + 32 * o + i + sub;
+                  if (8 * c < D)
+                    cp_async16(dst + key * 128 + (((c & 7) ^ (key & 7)) << 4),
+                               src >= 0 ? pool + src * step : pool, src >= 0 ? 16 : 0);
+                }
             }
             cp_async_commit();
-            // the tile before this one has landed: pass it on
-            if (tiles > 0) {
-              cp_async_wait<1>();
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar.full + 8 * ((stage + G::kStages - 1) % G::kStages));
+            if (tiles >= kLag) {
+              cp_async_wait<kLag>();
+              pass_on(kLag);
             }
+            copied = (copied << 1) | (there ? 0u : 1u);
             ++tiles;
             if (++stage == G::kStages) stage = 0, phase ^= 1;
           }
         }
       }
-      cp_async_wait<0>();
-      if (tiles > 0) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.full + 8 * ((stage + G::kStages - 1) % G::kStages));
+      if (tiles > 1) {
+        cp_async_wait<1>();
+        pass_on(2);
       }
-    } else if (warp == 12 && lane == 0) {
+      cp_async_wait<0>();
+      if (tiles > 0) pass_on(1);
+    } else if (warp == kMmaWarp && lane == 0) {
       // ---- the products
       constexpr bool kBf16 = T::kBf16;
       const uint32_t qk = mma_desc(kBf16, false, 128, G::kKeys);
-      const uint32_t pv = mma_desc(kBf16, true, 128, D);
-      uint32_t stage = 0, phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      const uint32_t pv = mma_desc(kBf16, true, 128, DC == 2 ? 128 : D);
+      uint32_t stage = 0, phase = 0, q_phase = 0, p_phase = 0;  // a bit for each query tile
       bool ok = any;
       const auto step = [&]() {
         if (++stage == G::kStages) stage = 0, phase ^= 1;
       };
-      const auto scores = [&](int tile, uint32_t k_smem) {
+      // operand descriptors of stage and tile 0; others are a 16-byte count away
+      const uint64_t q_desc = smem_desc(q_smem, 16, 1024);
+      const uint64_t k_desc = smem_desc(kv_smem, 16, 1024);
+      const uint64_t v_desc = smem_desc(kv_smem, G::kBlock, 1024);
+      const auto scores = [&](int tile, uint32_t at) {
+        const uint32_t dst = tmem + G::kS + tile * G::kSStep;
+        const uint64_t a = q_desc + tile * (DC * G::kQBytes >> 4);
+        const uint64_t b = k_desc + at * (G::kStage >> 4);
 #pragma unroll 1
-        for (int k = 0; k < D; k += 16) {
-          const uint32_t in = (k >> 6), off = (k & 63) * 2;
-          mma_ss(tmem + G::kS + tile * G::kSStep,
-                 smem_desc(q_smem + (tile * DC + in) * G::kQBytes + off, 16, 1024),
-                 smem_desc(k_smem + in * G::kBlock + off, 16, 1024), qk, k > 0);
-        }
+        for (int c = 0; 64 * c < D; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (64 * c + 16 * k < D)
+              mma_ss(dst, a + c * (G::kQBytes >> 4) + 2 * k, b + c * (G::kBlock >> 4) + 2 * k, qk,
+                     c > 0 || k > 0);
         mma_commit(bar.s_full + 8 * tile);
+      };
+      const auto outputs = [&](int tile, uint32_t at, bool add) {
+        const uint32_t dst = tmem + G::kO + tile * G::kOStep;
+        const uint32_t a = tmem + G::kP + tile * G::kPStep;
+        const uint64_t b = v_desc + at * (G::kStage >> 4);
+#pragma unroll
+        for (int k = 0; k < G::kKeys / 16; ++k)
+          mma_ts(dst, a + 8 * k, b + (k * 2048 >> 4), pv, k > 0 || add);
       };
       while (ok && w.next(p)) {
         const int active = w.it.rows > 128 ? 2 : 1;
@@ -445,10 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
         uint32_t k_stage = stage;
         step();
         for (int tile = 0; tile < active; ++tile) {
-          if (!(ok = mbar_wait(bar.q_full + 8 * tile, q_phase[tile], dead))) break;
-          q_phase[tile] ^= 1;
+          if (!(ok = mbar_wait(bar.q_full + 8 * tile, (q_phase >> tile) & 1, dead))) break;
+          q_phase ^= 1u << tile;
           tc_fence_after();
-          scores(tile, kv_smem + k_stage * G::kStage);
+          scores(tile, k_stage);
         }
         if (!ok) break;
         mma_commit(bar.empty + 8 * k_stage);
@@ -463,15 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
             step();
           }
           for (int tile = 0; tile < active; ++tile) {
-            if (!(ok = mbar_wait(bar.p_full + 8 * tile, p_phase[tile], dead))) break;
-            p_phase[tile] ^= 1;
+            if (!(ok = mbar_wait(bar.p_full + 8 * tile, (p_phase >> tile) & 1, dead))) break;
+            p_phase ^= 1u << tile;
             tc_fence_after();
-            const uint32_t v_smem = kv_smem + v_stage * G::kStage;
-#pragma unroll 1
-            for (int k = 0; k < G::kKeys; k += 16)
-              mma_ts(tmem + G::kO + tile * G::kOStep, tmem + G::kS + tile * G::kSStep + k / 2,
-                     smem_desc(v_smem + k * 128, G::kBlock, 1024), pv, u > w.first || k > 0);
-            if (more) scores(tile, kv_smem + k_stage * G::kStage);
+            outputs(tile, v_stage, u > w.first);
+            if (more) scores(tile, k_stage);
             else mma_commit(bar.o_full + 8 * tile);
           }
           if (!ok) break;
@@ -484,18 +603,63 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(AttnParams p) {
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    cudaDriverEntryPointQueryResult found;
+    void* f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// One half (K or V) of the layer's pool as [rows][heads][channels], copied in
+// boxes of `box` rows of one head's 64 channels, in the 128-byte swizzle;
+// channels behind the last are zeros.
+bool encode_map(CUtensorMap* map, const AttnParams& p, const uint16_t* half, int box, bool bf16) {
+  const cuuint64_t dims[3] = {cuuint64_t(p.dim), cuuint64_t(p.kv_heads),
+                              cuuint64_t(p.num_pages) * p.page_tokens};
+  const cuuint64_t strides[2] = {cuuint64_t(p.dim) * 2, cuuint64_t(p.dim) * p.kv_heads * 2};
+  const cuuint32_t shape[3] = {64, 1, cuuint32_t(box)}, ones[3] = {1, 1, 1};
+  return encode_fn()(map,
+                     bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                     const_cast<uint16_t*>(half), dims, strides, shape, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int DC>
 cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
+  using G = Geometry<DC>;
   const cudaError_t err = cudaFuncSetAttribute(
-      tile_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geometry<DC>::kSmem);
+      tile_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (err != cudaSuccess) return err;
-  tile_kernel<T, DC><<<p.tiles.ctas, kThreads, Geometry<DC>::kSmem, stream>>>(p);
+  // Keys that follow one another in a page for certain: the largest power of
+  // two in its size, as far as a warp's half of a tile.  The swizzle needs
+  // eight; smaller pages come row by row.
+  int box = p.page_tokens & -p.page_tokens;
+  box = std::min(box, G::kKeys / kLoadWarps);
+  CUtensorMap k_map{}, v_map{};
+  if (box < 8 || encode_fn() == nullptr) box = 0;
+  else if (!encode_map(&k_map, p, p.k_pool, box, T::kBf16) ||
+           !encode_map(&v_map, p, p.v_pool, box, T::kBf16))
+    box = 0;
+  tile_kernel<T, DC><<<p.tiles.ctas, kThreads, G::kSmem, stream>>>(p, k_map, v_map, box);
   return cudaGetLastError();
 }
 
