@@ -27,9 +27,10 @@ NVCC_FLAGS = ARCH + [
 
 CODEC_SOURCES = ["csrc/capi.cu", "csrc/encode.cu", "csrc/decode.cu", "csrc/static_ws.cu",
                  "csrc/context.cu", "csrc/capi_paged.cu", "csrc/tables.cu", "csrc/append.cu",
-                 "csrc/attend.cu", "csrc/attend_tile.cu"]
+                 "csrc/attend.cu", "csrc/attend_rows.cu", "csrc/attend_tile.cu",
+                 "csrc/attend_maps.cu"]
 CODEC_HEADERS = ["csrc/cg_common.cuh", "csrc/paged.cuh", "csrc/attend.cuh",
-                 "csrc/tcgen05.cuh"]
+                 "csrc/tcgen05.cuh", "csrc/kv_loader.cuh"]
 SYNTH_SOURCES = ["synth/kvsynth.cu"]
 
 LIB_CODEC = PKG / "libcachegen.so"

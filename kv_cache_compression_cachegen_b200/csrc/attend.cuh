@@ -21,12 +21,15 @@
 // every sum is fixed.
 #pragma once
 
+#include <cuda.h>  // tensor-map types only; the encoder is looked up at run time
+
 #include "paged.cuh"
 
 namespace cg {
 
 constexpr int kRowTile = 16;   // query rows of an item of the rows kernel (one matrix tile)
-constexpr int kRowKeys = 64;   // keys of a unit there
+constexpr int kRowKeys = 128;  // keys of a unit there
+constexpr int kScanSlots = 1024;  // slots of a line that every CTA sums up by itself
 
 // The line of work of one of the two kernels, in the workspace.
 struct Lane {
@@ -54,6 +57,7 @@ struct AttnParams {
   uint32_t q_flip;    // sign bits of a negative scale, applied to q
   int prefix_small;   // the rows of the whole batch fit the rows kernel
   int tiled;          // requests above the rows kernel's size may be there (max_q)
+  int planned;        // the lines are too long for that: a kernel before has summed them up
   Lane rows, tiles;
   // shared: items that one CTA finished, [own, prefix][num_tokens][q_heads][dim]
   float* whole;
@@ -147,6 +151,13 @@ __device__ __forceinline__ int slot_base(const AttnParams& p, int r) {
   return int(int64_t(a) * p.group / kTile) + r;
 }
 
+// What an item costs besides its units (queries, output, an empty pipeline), in
+// units, so that shares of many short items are not longer than others.
+template <int kTile>
+__host__ __device__ constexpr int item_cost() {
+  return kTile == kRowTile ? 1 : 2;
+}
+
 // The item of slot x and its units for each kv head; 0 where it holds no rows.
 template <int kTile, int kKeys>
 __device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it) {
@@ -189,7 +200,7 @@ __device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it) {
     it.span = span_of<kKeys>(it.req.row0 + t0, it.req.row0 + t1, p.window, p.sinks);
   }
   // an item without a visible key still has its rows to write
-  return it.span.units > 0 ? it.span.units : 1;
+  return (it.span.units > 0 ? it.span.units : 1) + item_cost<kTile>();
 }
 
 // Position of a row of an item among its keys (at the last one for the prefix).
@@ -213,6 +224,53 @@ __device__ __forceinline__ int pool_row(const AttnParams& p, const int32_t* tabl
   return page * p.page_tokens + (key - col * p.page_tokens);
 }
 
+// Units of one head before each slot of a line, and of the whole line behind
+// the last.  All threads of a block; blockDim.x at most 1024.
+template <int kTile, int kKeys>
+__device__ void sum_line(const AttnParams& p, int64_t* cum) {
+  __shared__ int64_t warp_sum[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int slots = total_slots<kTile>(p);
+  int64_t base = 0;
+  for (int x0 = 0; x0 < slots; x0 += blockDim.x) {
+    const int x = x0 + threadIdx.x;
+    Item it;
+    const int64_t own = x < slots ? slot_item<kTile, kKeys>(p, x, it) : 0;
+    int64_t sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(~0u, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    const int64_t w = lane < warps ? warp_sum[lane] : 0;
+    int64_t wi = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(~0u, wi, o);
+      if (lane >= o) wi += up;
+    }
+    const int64_t before = base + __shfl_sync(~0u, wi - w, warp) + sum - own;
+    if (x < slots) cum[x] = before;
+    base += __shfl_sync(~0u, wi, 31);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) cum[slots] = base;
+  __syncthreads();
+}
+
+// The slot that holds unit u of a line: the last one with heads * cum[x] <= u.
+__device__ __forceinline__ int slot_of(const int64_t* cum, int slots, int heads, int64_t u) {
+  int x = 0, hi = slots - 1;
+  while (x < hi) {
+    const int mid = (x + hi + 1) >> 1;
+    if (cum[mid] * heads <= u) x = mid;
+    else hi = mid - 1;
+  }
+  return x;
+}
+
 // One CTA's share of a line, item by item.
 template <int kTile, int kKeys>
 struct Walk {
@@ -223,22 +281,24 @@ struct Walk {
   int head, first, last, piece;
   bool whole;
 
-  __device__ __forceinline__ bool begin(const AttnParams& p, const Lane& lane) {
+  // All threads of the block; cum_s has room for kScanSlots + 1.
+  __device__ __forceinline__ bool begin(const AttnParams& p, const Lane& lane, int64_t* cum_s) {
     slots = total_slots<kTile>(p);
-    const int64_t units = lane.cum[slots] * p.kv_heads;
+    const int64_t* line = lane.cum;
+    if (!p.planned) {
+      sum_line<kTile, kKeys>(p, cum_s);
+      line = cum_s;
+      if (blockIdx.x == 0)  // for the join
+        for (int i = threadIdx.x; i <= slots; i += blockDim.x) lane.cum[i] = cum_s[i];
+    }
+    const int64_t units = line[slots] * p.kv_heads;
     const int ctas = shares_of(lane, units);
     if (int(blockIdx.x) >= ctas) return false;
     u = units * blockIdx.x / ctas;
     u_end = units * (blockIdx.x + 1) / ctas;
     share0 = u;
-    x = 0;  // the last slot with kv_heads * cum[x] <= u
-    int hi = slots - 1;
-    while (x < hi) {
-      const int mid = (x + hi + 1) >> 1;
-      if (lane.cum[mid] * p.kv_heads <= u) x = mid;
-      else hi = mid - 1;
-    }
-    cum = lane.cum[x];
+    x = slot_of(line, slots, p.kv_heads, u);
+    cum = line[x];
     return true;
   }
 
@@ -252,12 +312,14 @@ struct Walk {
       }
       head = int((u - cum * p.kv_heads) / cost);
       const int64_t item0 = cum * p.kv_heads + int64_t(head) * cost;
-      first = int(u - item0);
-      last = int((item0 + cost < u_end ? item0 + cost : u_end) - item0);
-      whole = first == 0 && last == cost;
+      const int from = int(u - item0);
+      const int to = int((item0 + cost < u_end ? item0 + cost : u_end) - item0);
+      whole = from == 0 && to == cost;
       piece = 2 * int(blockIdx.x) + (item0 >= share0 ? 1 : 0);
-      u = item0 + last;
-      if (it.span.units == 0) last = first;  // rows that see nothing
+      u = item0 + to;
+      // the first units of an item's cost stand for what an item takes by itself
+      first = max(0, from - item_cost<kTile>());
+      last = min(it.span.units, max(0, to - item_cost<kTile>()));
       return true;
     }
     return false;
@@ -288,9 +350,40 @@ __device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas) {
   return int(((u + 1) * ctas - 1) / units);
 }
 
-// attend_tile.cu
+// Programmatic dependent launch: let the next kernel of the stream start, and
+// wait for the one before to have finished and written its results.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem,
+                         cudaStream_t stream, bool early, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Tensor maps (attend_maps.cu) of one half (K or V) of the layer's pool in boxes
+// of `box` rows, and of the queries in boxes of 128 rows of a kv head.  False
+// where there is none for this geometry.
+struct KvMaps {
+  CUtensorMap k, v;
+  int box;  // 0: none
+};
+KvMaps kv_maps(const AttnParams& p, int most_rows, bool bf16);
+bool query_map(CUtensorMap* map, const AttnParams& p, bool bf16);
+
+// attend_tile.cu, attend_rows.cu
 int tile_rows(int dim);  // query rows of an item of the tile kernel
-int tile_keys(int dim);
 cudaError_t launch_tiles(const AttnParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_rows(const AttnParams& p, bool bf16, bool early, cudaStream_t stream);
 
 }  // namespace cg

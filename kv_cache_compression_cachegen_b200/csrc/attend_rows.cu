@@ -1,0 +1,359 @@
+// attend_rows.cu -- attention over the paged pool for few query rows a kv head:
+// single tokens with the heads of a group, a few tokens at most.
+//
+//     o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   s_j = (q . k_j) scale log2(e)
+//
+// in one pass over the keys with a running maximum m.  A row of K and V serves
+// at most 16 query rows, so the bytes of K and V bound it, and all that counts
+// is that enough of them are on their way: one CTA an SM, whose ring of stages
+// (kv_loader.cuh) takes most of the shared memory, about 190 KB.  Eight warps
+// read the stages, 16 keys of each unit a warp, with the 16-row matrix
+// instructions of a warp (fewer rows than the tensor-memory products want);
+// each warp keeps a maximum, sums and outputs of its own, joined once an item.
+#include <algorithm>
+
+#include "attend.cuh"
+#include "kv_loader.cuh"
+
+namespace cg {
+namespace {
+
+constexpr int kWarps = 8;  // that compute
+constexpr int kThreads = 32 * (kWarps + kLoadWarps);
+constexpr int kJoinBytes = 16 * 1024;
+constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
+static_assert(kRowKeys == 16 * kWarps, "each warp takes 16 keys of a unit");
+static_assert(kJoinBytes >= (kScanSlots + 1) * 8, "the line's sums lie there at first");
+
+template <int DC>
+struct Shape {
+  static constexpr int kStages = DC == 4 ? 3 : (DC == 2 ? 6 : 8);
+  static constexpr int kStage = DC * kRowKeys * 128;
+  static constexpr int kChannels = 64 * DC;
+  static constexpr int kJoinRows = std::min(16, kJoinBytes / (kWarps * kChannels * 4));
+  static constexpr int kSmem = kStages * kStage + kJoinBytes + 1024;
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void compute_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+
+template <typename T, int DC>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows_kernel(AttnParams p, const __grid_constant__ KvMaps maps) {
+  using S = Shape<DC>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[2 * S::kStages];
+  __shared__ uint32_t no_page[4][4];
+  __shared__ int dead_mem;
+  __shared__ float stat_m[kWarps][16], stat_l[kWarps][16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+  float* join = reinterpret_cast<float*>(smem_raw + (base - smem_addr(smem_raw)) +
+                                         S::kStages * S::kStage);
+  Ring ring{base, smem_addr(bars), smem_addr(bars) + 8 * S::kStages, no_page, &dead_mem};
+
+  let_next_start();
+  if (threadIdx.x == 0) {
+    dead_mem = 0;
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(ring.full + 8 * i, kLoadWarps);
+      mbar_init(ring.empty + 8 * i, kWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  Walk<kRowTile, kRowKeys> w;
+  const bool any = w.begin(p, p.rows, reinterpret_cast<int64_t*>(join));
+  __syncthreads();
+
+  if (any && warp >= kWarps) {
+    load_kv<DC, kRowTile, kRowKeys, S::kStages>(p, w, ring, &maps.k, &maps.v, maps.box,
+                                                warp - kWarps);
+  } else if (any) {
+    const int g = lane >> 2, c = lane & 3, D = p.dim;
+    // this lane's part of an ldmatrix address: K tiles by key, V tiles transposed
+    const int k_key = 16 * warp + ((lane >> 4) << 3) + (lane & 7), k_half = (lane >> 3) & 1;
+    const int v_key = 16 * warp + (((lane >> 3) & 1) << 3) + (lane & 7), v_half = lane >> 4;
+    const auto at = [](int key, int chunk) {  // byte of a 16-byte chunk in a tile
+      return uint32_t((chunk >> 3) * (kRowKeys * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4));
+    };
+    uint32_t stage = 0, phase = 0, unit_count = 0;
+    bool ok = true;
+    const auto release = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ring.empty + 8 * stage);
+      if (++stage == S::kStages) stage = 0, phase ^= 1;
+    };
+    while (w.next(p)) {
+      const Item& it = w.it;
+      const bool prefix = it.request < 0;
+      const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
+      const int tok0 = div_of(it.row, p.group_div);
+      const int tok1 = div_of(it.row + it.rows - 1, p.group_div);
+      const int pos0 = prefix ? it.req.row0 : it.req.row0 + tok0;
+      const int pos1 = prefix ? it.req.row0 : it.req.row0 + tok1;
+      // The two query rows of this lane's quad and their positions.
+      uint32_t qf[4 * DC][4];
+      int pos[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = it.row + g + 8 * i;
+        const int tok = div_of(row, p.group_div);
+        const bool real = g + 8 * i < it.rows;
+        pos[i] = row_position(p, it, row);
+        const uint16_t* src = p.q + int64_t(it.req.first + tok) * p.q_stride +
+                              int64_t(w.head * p.group + (row - tok * p.group)) * D + 2 * c;
+#pragma unroll
+        for (int k = 0; k < 4 * DC; ++k) {
+          uint32_t lo = 0, hi = 0;
+          if (real && 16 * k < D) {
+            lo = *reinterpret_cast<const uint32_t*>(src + 16 * k) ^ p.q_flip;
+            hi = *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) ^ p.q_flip;
+          }
+          qf[k][i] = lo;
+          qf[k][2 + i] = hi;
+        }
+      }
+      float acc[8 * DC][4];
+#pragma unroll
+      for (int j = 0; j < 8 * DC; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+      float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};  // m in log2 units
+
+      for (int u = w.first; u < w.last; ++u, ++unit_count) {
+        const int key0 = unit_key<kRowKeys>(it.span, u) + 16 * warp;
+        const bool used = key0 < it.span.hi && (key0 + 16 > it.span.lo || key0 < it.span.sink_end);
+        if (!(ok = mbar_wait(ring.full + 8 * stage, phase, ring.dead))) break;
+        // S = Q K^T for 16 keys, as two tiles of 8
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        uint32_t holes = 0;
+        if (used) {
+          const uint32_t tile = ring.smem + stage * S::kStage;
+#pragma unroll
+          for (int k = 0; k < 4 * DC; ++k)
+            if (16 * k < D) {
+              uint32_t b[4];
+              ldmatrix4(b, tile + at(k_key, 2 * k + k_half));
+              T::mma(s[0], qf[k], b[0], b[1]);
+              T::mma(s[1], qf[k], b[2], b[3]);
+            }
+          holes = (no_page[unit_count & 3][warp >> 1] >> (16 * (warp & 1))) & 0xFFFFu;
+        }
+        release();
+        bool mixed = false;
+        uint32_t a[4] = {0, 0, 0, 0};
+        if (used) {
+          // s[t][e]: row e / 2, key 2 c + (e & 1) + 8 t of the sixteen
+          const bool full = holes == 0 && key0 + 15 <= pos0 &&
+                            (window == 0 || pos1 - key0 < window || key0 + 15 < sinks);
+          float most[2] = {kNegInf, kNegInf};
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[t][e] *= p.scale_log2;
+              if (!full) {
+                const int j = 2 * c + (e & 1) + 8 * t;
+                if (((holes >> j) & 1) || !sees(key0 + j, pos[e >> 1], window, sinks))
+                  s[t][e] = kNegInf;
+              }
+              most[e >> 1] = fmaxf(most[e >> 1], s[t][e]);
+            }
+          mixed = !full && tok0 != tok1;
+          // The maximum moves only when a score passes it by 2^8: weights up to
+          // that are in range of both types, and nothing is rescaled until then.
+          if (__any_sync(~0u, most[0] > m[0] + kSlack || most[1] > m[1] + kSlack)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              most[i] = fmaxf(most[i], __shfl_xor_sync(~0u, most[i], 1));
+              most[i] = fmaxf(most[i], __shfl_xor_sync(~0u, most[i], 2));
+              const float next = fmaxf(m[i], most[i]);
+              const float f = m[i] == next ? 1.f : exp2_fast(m[i] - next);
+              m[i] = next;
+              l[i] *= f;
+#pragma unroll
+              for (int j = 0; j < 8 * DC; ++j) acc[j][2 * i] *= f, acc[j][2 * i + 1] *= f;
+            }
+          }
+          float pr[2][4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              pr[t][e] = s[t][e] == kNegInf ? 0.f : exp2_fast(s[t][e] - m[e >> 1]);
+              l[e >> 1] += pr[t][e];
+            }
+          // Rounded to the pool's type for the product with V: half a step of it
+          // relative to each weight; the sum l is not.
+          a[0] = T::pack(pr[0][0], pr[0][1]);
+          a[1] = T::pack(pr[0][2], pr[0][3]);
+          a[2] = T::pack(pr[1][0], pr[1][1]);
+          a[3] = T::pack(pr[1][2], pr[1][3]);
+        }
+        if (!(ok = mbar_wait(ring.full + 8 * stage, phase, ring.dead))) break;
+        if (used) {
+          const uint32_t tile = ring.smem + stage * S::kStage;
+          // A weight of zero does not hide a value that is not finite.  Where rows
+          // of several positions share such a value, each position takes the
+          // product by itself, with the values it does not see put to zero.
+          bool bad = false;
+          if (mixed) {
+#pragma unroll 1
+            for (int k = 0; 16 * k < D; ++k) {
+              uint32_t b[4];
+              ldmatrix4_t(b, tile + at(v_key, 2 * k + v_half));
+              bad |= T::not_finite(b[0]) | T::not_finite(b[1]) | T::not_finite(b[2]) |
+                     T::not_finite(b[3]);
+            }
+            bad = __any_sync(~0u, bad);
+          }
+          if (!bad) {
+#pragma unroll
+            for (int k = 0; k < 4 * DC; ++k)
+              if (16 * k < D) {
+                uint32_t b[4];
+                ldmatrix4_t(b, tile + at(v_key, 2 * k + v_half));
+                T::mma(acc[2 * k], a, b[0], b[1]);
+                T::mma(acc[2 * k + 1], a, b[2], b[3]);
+              }
+          } else {
+            for (int here = pos0; here <= pos1; ++here) {
+              uint32_t keep[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                keep[h] = (sees(key0 + 2 * c + 8 * h, here, window, sinks) ? 0xFFFFu : 0u) |
+                          (sees(key0 + 2 * c + 1 + 8 * h, here, window, sinks) ? 0xFFFF0000u : 0u);
+#pragma unroll
+              for (int k = 0; k < 4 * DC; ++k)
+                if (16 * k < D) {
+                  uint32_t b[4];
+                  ldmatrix4_t(b, tile + at(v_key, 2 * k + v_half));
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+                    T::mma(part, a, b[2 * h] & keep[0], b[2 * h + 1] & keep[1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      if (pos[e >> 1] == here) acc[2 * k + h][e] += part[e];
+                  }
+                }
+            }
+          }
+        }
+        release();
+      }
+
+      // Join the warps: sums over the quad, then under the common maximum.
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(~0u, l[i], 1);
+        l[i] += __shfl_xor_sync(~0u, l[i], 2);
+        if (c == 0) {
+          stat_m[warp][g + 8 * i] = m[i];
+          stat_l[warp][g + 8 * i] = l[i];
+        }
+      }
+      compute_sync();
+      float f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float top = kNegInf;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, stat_m[k][g + 8 * i]);
+        f[i] = weight_of(m[i], top);
+      }
+      const int quads = D / 4;
+      for (int r0 = 0; r0 < it.rows; r0 += S::kJoinRows) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = g + 8 * i - r0;
+          if (row < 0 || row >= S::kJoinRows) continue;
+          float* dst = join + (warp * S::kJoinRows + row) * S::kChannels + 2 * c;
+#pragma unroll
+          for (int j = 0; j < 8 * DC; ++j)
+            *reinterpret_cast<float2*>(dst + 8 * j) =
+                make_float2(acc[j][2 * i] * f[i], acc[j][2 * i + 1] * f[i]);
+        }
+        compute_sync();
+        // thread: four channels of a row
+        const int rows = min(S::kJoinRows, it.rows - r0);
+        for (int i = threadIdx.x; i < rows * quads; i += 32 * kWarps) {
+          const int r = i / quads, row = r0 + r, d = (i - r * quads) * 4;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          float mm = kNegInf, ll = 0.f;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(
+                join + (k * S::kJoinRows + r) * S::kChannels + d);
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            mm = fmaxf(mm, stat_m[k][row]);
+          }
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) ll += stat_l[k][row] * weight_of(stat_m[k][row], mm);
+          const int tok = div_of(it.row + row, p.group_div);
+          const int64_t t = it.req.first + tok;
+          const int qh = w.head * p.group + it.row + row - tok * p.group;
+          if (!w.whole) {
+            const int64_t to = int64_t(w.piece) * kRowTile + row;
+            *reinterpret_cast<float4*>(p.rows.pieces + to * D + d) = o;
+            if (d == 0) p.rows.stats[to] = make_float2(mm, ll);
+          } else if (p.shared) {
+            const int64_t to = (int64_t(prefix) * p.num_tokens + t) * p.q_heads + qh;
+            *reinterpret_cast<float4*>(p.whole + to * D + d) = o;
+            if (d == 0) p.whole_stats[to] = make_float2(mm, ll);
+          } else {
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            *reinterpret_cast<uint2*>(p.out + t * p.out_stride + int64_t(qh) * D + d) =
+                make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv));
+            if (d == 0 && p.lse != nullptr) p.lse[t * p.q_heads + qh] = log_sum(mm, ll);
+          }
+        }
+        compute_sync();  // join and the statistics are written again
+      }
+      // A wait that ran out: all warps are at this item and leave together.
+      if (*ring.dead != 0) break;
+    }
+    if (!ok && lane == 0) report(p.status, CG_ERR_CUDA);
+  }
+  // this kernel may have started before the tile kernel was done; the join
+  // waits for this one, and so for both
+  wait_for_previous();
+}
+
+template <typename T, int DC>
+cudaError_t launch(const AttnParams& p, bool early, cudaStream_t stream) {
+  using S = Shape<DC>;
+  const cudaError_t err = cudaFuncSetAttribute(
+      rows_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (err != cudaSuccess) return err;
+  return launch_after(rows_kernel<T, DC>, p.rows.ctas, kThreads, S::kSmem, stream, early, p,
+                      kv_maps(p, kRowKeys / kLoadWarps, T::kBf16));
+}
+
+template <typename T>
+cudaError_t launch_type(const AttnParams& p, bool early, cudaStream_t stream) {
+  if (p.dim <= 64) return launch<T, 1>(p, early, stream);
+  if (p.dim <= 128) return launch<T, 2>(p, early, stream);
+  return launch<T, 4>(p, early, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rows(const AttnParams& p, bool bf16, bool early, cudaStream_t stream) {
+  return bf16 ? launch_type<BF16>(p, early, stream) : launch_type<F16>(p, early, stream);
+}
+
+}  // namespace cg

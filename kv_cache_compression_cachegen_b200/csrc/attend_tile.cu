@@ -5,11 +5,9 @@
 //   warps 0-3, 4-7   softmax of query tile 0 and 1 (128 rows each, a row a
 //                    thread): scores out of tensor memory, running maximum and
 //                    sum, weights back into tensor memory; output of the item
-//   warps 10, 11     K and V from the pages to shared memory, in the 128-byte
-//                    swizzle: by TMA where all of a warp's half of a tile can be
-//                    seen and lies in runs of eight rows or more, else row by row
-//                    (cp.async; a page may end anywhere in a tile) with zeros for
-//                    what no row of the item sees
+//   warps 10, 11     K and V from the pages to shared memory (kv_loader.cuh)
+//   warp 9           queries to shared memory, as soon as the last product with
+//                    the item's before has read them
 //   warp 8           one thread issues the products:
 //                      S = Q K^T   both operands in shared memory
 //                      O += P V    P in tensor memory, V along its channels
@@ -19,18 +17,14 @@
 // The running maximum m moves only when a score passes it by 2^8: until then
 // weights up to 2^8 are in range of fp16 and bf16 alike, nothing is lost, and
 // the output need not be read back from tensor memory to be rescaled.
-#include <cuda.h>  // tensor-map types only; the encoder is looked up at run time
-
-#include <algorithm>
-
 #include "attend.cuh"
-#include "tcgen05.cuh"
+#include "kv_loader.cuh"
 
 namespace cg {
 namespace {
 
 constexpr int kThreads = 384;  // 168 registers a thread: a softmax thread holds 128 scores
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoadWarps = 2;
+constexpr int kMmaWarp = 8, kQueryWarp = 9, kLoadWarp = 10;
 constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
 
 template <int DC>
@@ -57,7 +51,7 @@ struct Geometry {
 };
 
 struct Bars {
-  uint32_t full, empty, q_full, s_full, p_full, o_full;  // each the first of its array
+  uint32_t q_full, q_free, s_full, p_full, o_full;  // each the first of its two
 };
 
 // 2^x of two values without the special-function unit, which alone would take
@@ -154,35 +148,38 @@ __device__ __forceinline__ void recompute_row(const AttnParams& p, const Item& i
 
 template <typename T, int DC>
 __global__ void __launch_bounds__(kThreads, 1)
-    tile_kernel(AttnParams p, const __grid_constant__ CUtensorMap k_map,
-                const __grid_constant__ CUtensorMap v_map, int box) {
+    tile_kernel(AttnParams p, const __grid_constant__ KvMaps maps,
+                const __grid_constant__ CUtensorMap q_map, int by_map) {
   using G = Geometry<DC>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars_mem[2 * G::kStages + 8];
+  __shared__ uint64_t bars_mem[2 * G::kStages + 10];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_mem;
-  __shared__ uint32_t no_page[4][4];  // keys of a unit whose page is not in the pool
+  __shared__ uint32_t no_page[4][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t q_smem = base;
   const uint32_t kv_smem = base + G::kTiles * DC * G::kQBytes;
   volatile int* dead = &dead_mem;
+  const uint32_t bars = smem_addr(bars_mem);
+  const Ring ring{kv_smem, bars, bars + 8 * G::kStages, no_page, &dead_mem};
   Bars bar;
-  bar.full = smem_addr(bars_mem);
-  bar.empty = bar.full + 8 * G::kStages;
-  bar.q_full = bar.empty + 8 * G::kStages;
-  bar.s_full = bar.q_full + 16;
+  bar.q_full = ring.empty + 8 * G::kStages;
+  bar.q_free = bar.q_full + 16;
+  bar.s_full = bar.q_free + 16;
   bar.p_full = bar.s_full + 16;
   bar.o_full = bar.p_full + 16;
 
+  let_next_start();
   if (threadIdx.x == 0) {
     dead_mem = 0;
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(bar.full + 8 * i, kLoadWarps);
-      mbar_init(bar.empty + 8 * i, 1);
+      mbar_init(ring.full + 8 * i, kLoadWarps);
+      mbar_init(ring.empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar.q_full + 8 * i, 4);
+      mbar_init(bar.q_full + 8 * i, 1);
+      mbar_init(bar.q_free + 8 * i, 1);
       mbar_init(bar.s_full + 8 * i, 1);
       mbar_init(bar.p_full + 8 * i, 4);
       mbar_init(bar.o_full + 8 * i, 1);
@@ -190,13 +187,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tmem_alloc(smem_addr(&tmem_slot), 512);
+  Walk<G::kRows, G::kKeys> w;
+  const bool any = w.begin(p, p.tiles, reinterpret_cast<int64_t*>(smem_raw));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-
-  Walk<G::kRows, G::kKeys> w;
-  const bool any = w.begin(p, p.tiles);
   const int D = p.dim;
 
   if (warp < 8) {
@@ -223,33 +219,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
       float m = kNegInf, l = 0.f;
       bool mixed = false;  // some unit had keys that a row does not see
-      if (w.first < w.last) {
-        // Q: eight lanes a row, so that a row's bytes are read together
-        for (int i = 0; i < 32; i += 4) {
-          const int rr = 32 * (warp & 3) + i + (lane >> 3);
-          const bool have = 128 * tile + rr < it.rows;
-          const int qrow = it.row + 128 * tile + rr;
-          const int qtok = div_of(qrow, p.group_div);
-          const uint16_t* src = p.q + int64_t(it.req.first + qtok) * p.q_stride +
-                                int64_t(w.head * p.group + qrow - qtok * p.group) * D;
-#pragma unroll
-          for (int b = 0; b < DC; ++b) {
-            const int c = lane & 7;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (have && 64 * b + 8 * c < D)
-              v = *reinterpret_cast<const uint4*>(src + 64 * b + 8 * c);
-            v.x ^= p.q_flip, v.y ^= p.q_flip, v.z ^= p.q_flip, v.w ^= p.q_flip;
-            const uint32_t dst = q_smem + (tile * DC + b) * G::kQBytes + rr * 128 +
-                                 ((c ^ (rr & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y),
-                         "r"(v.z), "r"(v.w)
-                         : "memory");
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.q_full + 8 * tile);
-      }
       for (int u = w.first; u < w.last; ++u) {
         if (!(ok = mbar_wait(bar.s_full + 8 * tile, s_phase, dead))) break;
         s_phase ^= 1;
@@ -411,121 +380,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && any && tile < G::kTiles && lane == 0) report(p.status, CG_ERR_CUDA);
   } else {
     if (warp >= kLoadWarp) {
-      // ---- K and V to shared memory
-      const int wk = warp - kLoadWarp;
-      constexpr int kLanes = 8 * DC;            // lanes of a row (16 bytes each)
-      constexpr int kPer = 32 / kLanes;         // rows a warp copies at a time
-      constexpr int kMine = G::kKeys / kLoadWarps;  // rows of a tile that are this warp's
-      constexpr int kOwn = kMine / 32;              // of these, a lane's
-      const int c = lane % kLanes, sub = lane / kLanes;
-      const int64_t step = int64_t(p.kv_heads) * D;
-      uint32_t stage = 0, phase = 1, tiles = 0, unit_count = 0;
-      uint32_t copied = 0;  // the latest tiles, a bit each: this warp's half came by cp.async
+      if (any)
+        load_kv<DC, G::kRows, G::kKeys, G::kStages>(p, w, ring, &maps.k, &maps.v, maps.box,
+                                                    warp - kLoadWarp);
+    } else if (warp == kQueryWarp) {
+      // ---- queries
+      uint32_t q_phase = 3;  // a bit for each query tile
       bool ok = any;
-      // Halves that came by cp.async are passed on kLag tiles behind the one that
-      // is being asked for, when they have landed, so that more are on their way.
-      constexpr int kLag = 2;
-      const auto pass_on = [&](uint32_t behind) {
-        if ((copied >> (behind - 1)) & 1) {
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0)
-            mbar_arrive(bar.full + 8 * ((stage + G::kStages - behind) % G::kStages));
-        }
-      };
-      const int boxes = box > 0 ? kMine / box * DC : 0;  // TMA boxes of the warp's half of a tile
       while (ok && w.next(p)) {
         const Item& it = w.it;
-        const bool prefix = it.request < 0;
-        const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
-        const int64_t col = int64_t(w.head) * D + 8 * c;
-        // Lane i has the warp's keys i, i + 32, ... of the unit; their pages are
-        // looked up a unit ahead.  -2: no row of the item sees the key.
-        int key_ahead[kOwn], page_ahead[kOwn], mine[kOwn];
-        const auto look_up = [&](int u) {
+        if (w.first >= w.last) continue;
+        for (int tile = 0; tile < (it.rows > 128 ? 2 : 1); ++tile) {
+          if (!(ok = mbar_wait(bar.q_free + 8 * tile, (q_phase >> tile) & 1, dead))) break;
+          q_phase ^= 1u << tile;
+          const uint32_t dst = q_smem + tile * DC * G::kQBytes;
+          const int row0 = it.row + 128 * tile;
+          if (by_map) {
+            // rows behind the item's are other tokens' or zeros, and are not used
+            if (lane == 0) {
+              mbar_expect(bar.q_full + 8 * tile, DC * G::kQBytes);
+              for (int b = 0; b < DC; ++b)
+                tma_load3(dst + b * G::kQBytes, &q_map, 64 * b, w.head * p.group,
+                          it.req.first + div_of(row0, p.group_div), bar.q_full + 8 * tile);
+            }
+            continue;
+          }
+#pragma unroll 4
+          for (int i = 0; i < 128; i += 4) {  // eight lanes a row
+            const int r = i + (lane >> 3), c = lane & 7, row = row0 + r;
+            const int tok = div_of(row, p.group_div);
+            const uint16_t* src = p.q + int64_t(it.req.first + tok) * p.q_stride +
+                                  int64_t(w.head * p.group + row - tok * p.group) * D + 8 * c;
 #pragma unroll
-          for (int i = 0; i < kOwn; ++i) {
-            page_ahead[i] = -2;
-            key_ahead[i] = 0;
-            if (u < w.last) {
-              const int key = unit_key<G::kKeys>(it.span, u) + kMine * wk + 32 * i + lane;
-              if (key < it.span.hi && (key >= it.span.lo || key < it.span.sink_end))
-                page_ahead[i] = max(-1, __ldg(table + div_of(key, p.page_div)));
-              key_ahead[i] = key;
+            for (int b = 0; b < DC; ++b) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (128 * tile + r < it.rows && 64 * b + 8 * c < D)
+                v = *reinterpret_cast<const uint4*>(src + 64 * b);
+              v.x ^= p.q_flip, v.y ^= p.q_flip, v.z ^= p.q_flip, v.w ^= p.q_flip;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               dst + b * G::kQBytes + r * 128 + ((c ^ (r & 7)) << 4)),
+                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                           : "memory");
             }
           }
-        };
-        look_up(w.first);
-        for (int u = w.first; ok && u < w.last; ++u, ++unit_count) {
-          uint32_t holes[kOwn];
-          bool there = box > 0;  // every key of the warp's half can be read
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i) {
-            const bool hole = page_ahead[i] == -1 || page_ahead[i] >= p.num_pages;
-            mine[i] = -1;
-            if (page_ahead[i] >= 0 && !hole)
-              mine[i] = page_ahead[i] * p.page_tokens +
-                        (key_ahead[i] - div_of(key_ahead[i], p.page_div) * p.page_tokens);
-            holes[i] = __ballot_sync(~0u, hole);
-            there = there && mine[i] >= 0;
-            if (holes[i] != 0 && lane == 0) report(p.status, CG_ERR_MISMATCH);
-          }
-          there = __all_sync(~0u, there);
-          look_up(u + 1);
-          for (int kv = 0; kv < 2; ++kv) {
-            if (!(ok = mbar_wait(bar.empty + 8 * stage, phase, dead))) break;
-            if (kv == 0 && lane == 0) {
-#pragma unroll
-              for (int i = 0; i < kOwn; ++i) no_page[unit_count & 3][wk * kOwn + i] = holes[i];
-            }
-            __syncwarp();
-            const uint32_t tile_smem = kv_smem + stage * G::kStage;
-            if (there) {
-              // whole boxes of keys that follow one another in a page
-              if (lane == 0) mbar_expect(bar.full + 8 * stage, kMine * 128 * DC);
-              __syncwarp();
-              for (int i0 = 0; i0 < boxes; i0 += 32) {
-                const int i = i0 + lane, b = i % DC, key = i / DC * box;
-                int row = __shfl_sync(~0u, mine[0], key & 31);
-                if constexpr (kOwn == 2) {
-                  const int upper = __shfl_sync(~0u, mine[kOwn - 1], key & 31);
-                  if (key >= 32) row = upper;
-                }
-                if (i < boxes)
-                  tma_load3(tile_smem + b * G::kBlock + (kMine * wk + key) * 128,
-                            kv ? &v_map : &k_map, 64 * b, w.head, row, bar.full + 8 * stage);
-              }
-            } else {
-              const uint16_t* pool = (kv ? p.v_pool : p.k_pool) + col;
-              const uint32_t dst = tile_smem + (c >> 3) * G::kBlock;
-#pragma unroll
-              for (int o = 0; o < kOwn; ++o)
-#pragma unroll 8
-                for (int i = 0; i < 32; i += kPer) {
-                  const int src = __shfl_sync(~0u, mine[o], i + sub);
-                  const int key = kMine * wk + 32 * o + i + sub;
-                  if (8 * c < D)
-                    cp_async16(dst + key * 128 + (((c & 7) ^ (key & 7)) << 4),
-                               src >= 0 ? pool + src * step : pool, src >= 0 ? 16 : 0);
-                }
-            }
-            cp_async_commit();
-            if (tiles >= kLag) {
-              cp_async_wait<kLag>();
-              pass_on(kLag);
-            }
-            copied = (copied << 1) | (there ? 0u : 1u);
-            ++tiles;
-            if (++stage == G::kStages) stage = 0, phase ^= 1;
-          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.q_full + 8 * tile);
         }
       }
-      if (tiles > 1) {
-        cp_async_wait<1>();
-        pass_on(2);
-      }
-      cp_async_wait<0>();
-      if (tiles > 0) pass_on(1);
     } else if (warp == kMmaWarp && lane == 0) {
       // ---- the products
       constexpr bool kBf16 = T::kBf16;
@@ -540,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q_desc = smem_desc(q_smem, 16, 1024);
       const uint64_t k_desc = smem_desc(kv_smem, 16, 1024);
       const uint64_t v_desc = smem_desc(kv_smem, G::kBlock, 1024);
-      const auto scores = [&](int tile, uint32_t at) {
+      const auto scores = [&](int tile, uint32_t at, bool final) {
         const uint32_t dst = tmem + G::kS + tile * G::kSStep;
         const uint64_t a = q_desc + tile * (DC * G::kQBytes >> 4);
         const uint64_t b = k_desc + at * (G::kStage >> 4);
@@ -552,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ss(dst, a + c * (G::kQBytes >> 4) + 2 * k, b + c * (G::kBlock >> 4) + 2 * k, qk,
                      c > 0 || k > 0);
         mma_commit(bar.s_full + 8 * tile);
+        if (final) mma_commit(bar.q_free + 8 * tile);
       };
       const auto outputs = [&](int tile, uint32_t at, bool add) {
         const uint32_t dst = tmem + G::kO + tile * G::kOStep;
@@ -564,24 +467,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && w.next(p)) {
         const int active = w.it.rows > 128 ? 2 : 1;
         if (w.first >= w.last) continue;
-        if (!(ok = mbar_wait(bar.full + 8 * stage, phase, dead))) break;
+        if (!(ok = mbar_wait(ring.full + 8 * stage, phase, dead))) break;
         uint32_t k_stage = stage;
         step();
         for (int tile = 0; tile < active; ++tile) {
           if (!(ok = mbar_wait(bar.q_full + 8 * tile, (q_phase >> tile) & 1, dead))) break;
           q_phase ^= 1u << tile;
           tc_fence_after();
-          scores(tile, k_stage);
+          scores(tile, k_stage, w.first + 1 == w.last);
         }
         if (!ok) break;
-        mma_commit(bar.empty + 8 * k_stage);
+        mma_commit(ring.empty + 8 * k_stage);
         for (int u = w.first; ok && u < w.last; ++u) {
           const bool more = u + 1 < w.last;
-          if (!(ok = mbar_wait(bar.full + 8 * stage, phase, dead))) break;
+          if (!(ok = mbar_wait(ring.full + 8 * stage, phase, dead))) break;
           const uint32_t v_stage = stage;
           step();
           if (more) {
-            if (!(ok = mbar_wait(bar.full + 8 * stage, phase, dead))) break;
+            if (!(ok = mbar_wait(ring.full + 8 * stage, phase, dead))) break;
             k_stage = stage;
             step();
           }
@@ -590,12 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             p_phase ^= 1u << tile;
             tc_fence_after();
             outputs(tile, v_stage, u > w.first);
-            if (more) scores(tile, k_stage);
+            if (more) scores(tile, k_stage, u + 2 == w.last);
             else mma_commit(bar.o_full + 8 * tile);
           }
           if (!ok) break;
-          mma_commit(bar.empty + 8 * v_stage);
-          if (more) mma_commit(bar.empty + 8 * k_stage);
+          mma_commit(ring.empty + 8 * v_stage);
+          if (more) mma_commit(ring.empty + 8 * k_stage);
         }
       }
     }
@@ -609,57 +512,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    cudaDriverEntryPointQueryResult found;
-    void* f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
-
-// One half (K or V) of the layer's pool as [rows][heads][channels], copied in
-// boxes of `box` rows of one head's 64 channels, in the 128-byte swizzle;
-// channels behind the last are zeros.
-bool encode_map(CUtensorMap* map, const AttnParams& p, const uint16_t* half, int box, bool bf16) {
-  const cuuint64_t dims[3] = {cuuint64_t(p.dim), cuuint64_t(p.kv_heads),
-                              cuuint64_t(p.num_pages) * p.page_tokens};
-  const cuuint64_t strides[2] = {cuuint64_t(p.dim) * 2, cuuint64_t(p.dim) * p.kv_heads * 2};
-  const cuuint32_t shape[3] = {64, 1, cuuint32_t(box)}, ones[3] = {1, 1, 1};
-  return encode_fn()(map,
-                     bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                     const_cast<uint16_t*>(half), dims, strides, shape, ones,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename T, int DC>
 cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   using G = Geometry<DC>;
   const cudaError_t err = cudaFuncSetAttribute(
       tile_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (err != cudaSuccess) return err;
-  // Keys that follow one another in a page for certain: the largest power of
-  // two in its size, as far as a warp's half of a tile.  The swizzle needs
-  // eight; smaller pages come row by row.
-  int box = p.page_tokens & -p.page_tokens;
-  box = std::min(box, G::kKeys / kLoadWarps);
-  CUtensorMap k_map{}, v_map{};
-  if (box < 8 || encode_fn() == nullptr) box = 0;
-  else if (!encode_map(&k_map, p, p.k_pool, box, T::kBf16) ||
-           !encode_map(&v_map, p, p.v_pool, box, T::kBf16))
-    box = 0;
-  tile_kernel<T, DC><<<p.tiles.ctas, kThreads, G::kSmem, stream>>>(p, k_map, v_map, box);
+  CUtensorMap q_map{};
+  const int by_map = query_map(&q_map, p, T::kBf16);
+  tile_kernel<T, DC><<<p.tiles.ctas, kThreads, G::kSmem, stream>>>(
+      p, kv_maps(p, G::kKeys / kLoadWarps, T::kBf16), q_map, by_map);
   return cudaGetLastError();
 }
 
@@ -673,7 +535,6 @@ cudaError_t launch_type(const AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 int tile_rows(int dim) { return dim <= 128 ? Geometry<2>::kRows : Geometry<4>::kRows; }
-int tile_keys(int dim) { return dim <= 128 ? Geometry<2>::kKeys : Geometry<4>::kKeys; }
 
 cudaError_t launch_tiles(const AttnParams& p, bool bf16, cudaStream_t stream) {
   return bf16 ? launch_type<BF16>(p, stream) : launch_type<F16>(p, stream);
