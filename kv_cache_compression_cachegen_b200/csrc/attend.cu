@@ -95,10 +95,10 @@ __device__ __forceinline__ void join_cut(const AttnParams& p, const Lane& line, 
   const int64_t units = line.cum[slots] * H;
   const int ctas = shares_of(line, units);
   if (cut >= ctas) return;
-  const int64_t u = units * cut / ctas;
+  const int64_t u = share_of(cut, units, ctas);
   const int x = slot_of(line.cum, slots, H, u);
   const int64_t cum = line.cum[x], cost = line.cum[x + 1] - cum;
-  const int head = int((u - cum * H) / cost);
+  const int head = int(uint32_t(u - cum * H) / uint32_t(cost));
   const int64_t item0 = cum * H + head * cost;
   if (item0 == u) return;  // between two items
   Part part[1];
@@ -154,16 +154,11 @@ __device__ __forceinline__ Part find_part(const AttnParams& p, const Lane& line,
 template <typename T, int kTile>
 __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(AttnParams p) {
   wait_for_previous();
-  const int64_t row_id = int64_t(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  if (row_id >= int64_t(p.num_tokens) * p.q_heads) return;
-  const int t = int(row_id / p.q_heads), qh = int(row_id - int64_t(t) * p.q_heads);
+  const int row_id = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (row_id >= p.num_tokens * p.q_heads) return;
+  const int t = row_id / p.q_heads, qh = row_id - t * p.q_heads;
   if (t >= p.q_starts[p.num_requests]) return;
-  int lo = 0, hi = p.num_requests - 1;  // the last request that starts at or before t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.q_starts[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
+  const int lo = request_of(p, t);
   Request req;
   if (!load_request(p, lo, req) || t < req.first || t >= req.first + req.tokens) return;
   const int head = div_of(qh, p.group_div), member = qh - head * p.group;

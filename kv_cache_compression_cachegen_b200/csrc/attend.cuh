@@ -208,6 +208,20 @@ __device__ __forceinline__ int row_position(const AttnParams& p, const Item& it,
   return it.request < 0 ? it.req.row0 : it.req.row0 + div_of(row, p.group_div);
 }
 
+// The last request that starts at or before packed row t; all lanes of a warp.
+__device__ __forceinline__ int request_of(const AttnParams& p, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.num_requests;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool before = lane * step < n && (lane == 0 || p.q_starts[at] <= t);
+    const int k = __popc(__ballot_sync(~0u, before)) - 1;  // starts do not fall
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
 // CTAs that get a share: no share is empty.
 __device__ __forceinline__ int shares_of(const Lane& lane, int64_t units) {
   return units < lane.ctas ? int(units) : lane.ctas;
@@ -222,6 +236,20 @@ __device__ __forceinline__ int pool_row(const AttnParams& p, const int32_t* tabl
     return -1;
   }
   return page * p.page_tokens + (key - col * p.page_tokens);
+}
+
+// CTA that holds unit u when `units` are dealt to `ctas`: share c is
+// [c * units / ctas, (c + 1) * units / ctas).
+__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas) {
+  if (units < (1 << 24))  // 32 bits do, for fewer than 256 CTAs
+    return int((uint32_t(u + 1) * uint32_t(ctas) - 1) / uint32_t(units));
+  return int(((u + 1) * ctas - 1) / units);
+}
+
+// First unit of share c.
+__device__ __forceinline__ int64_t share_of(int c, int64_t units, int ctas) {
+  if (units < (1 << 24)) return uint32_t(units) * uint32_t(c) / uint32_t(ctas);
+  return units * c / ctas;
 }
 
 // Units of one head before each slot of a line, and of the whole line behind
@@ -294,8 +322,8 @@ struct Walk {
     const int64_t units = line[slots] * p.kv_heads;
     const int ctas = shares_of(lane, units);
     if (int(blockIdx.x) >= ctas) return false;
-    u = units * blockIdx.x / ctas;
-    u_end = units * (blockIdx.x + 1) / ctas;
+    u = share_of(blockIdx.x, units, ctas);
+    u_end = share_of(blockIdx.x + 1, units, ctas);
     share0 = u;
     x = slot_of(line, slots, p.kv_heads, u);
     cum = line[x];
@@ -310,7 +338,7 @@ struct Walk {
         ++x;
         continue;
       }
-      head = int((u - cum * p.kv_heads) / cost);
+      head = int(uint32_t(u - cum * p.kv_heads) / uint32_t(cost));  // a slot's units fit 31 bits
       const int64_t item0 = cum * p.kv_heads + int64_t(head) * cost;
       const int from = int(u - item0);
       const int to = int((item0 + cost < u_end ? item0 + cost : u_end) - item0);
@@ -342,12 +370,6 @@ constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float log_sum(float m, float l) {
   return l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718056f;
-}
-
-// CTA that holds unit u when `units` are dealt to `ctas`: share c is
-// [c * units / ctas, (c + 1) * units / ctas).
-__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas) {
-  return int(((u + 1) * ctas - 1) / units);
 }
 
 // Programmatic dependent launch: let the next kernel of the stream start, and

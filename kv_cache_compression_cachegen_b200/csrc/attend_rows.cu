@@ -79,8 +79,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   if (any && warp >= kWarps) {
-    load_kv<DC, kRowTile, kRowKeys, S::kStages>(p, w, ring, &maps.k, &maps.v, maps.box,
-                                                warp - kWarps);
+    if (maps.box > 0)
+      load_boxes<DC, kRowTile, kRowKeys, S::kStages>(p, w, ring, &maps.k, &maps.v, maps.box,
+                                                     warp - kWarps);
+    else
+      load_kv<DC, kRowTile, kRowKeys, S::kStages>(p, w, ring, nullptr, nullptr, 0, warp - kWarps);
   } else if (any) {
     const int g = lane >> 2, c = lane & 3, D = p.dim;
     // this lane's part of an ldmatrix address: K tiles by key, V tiles transposed
@@ -96,35 +99,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(ring.empty + 8 * stage);
       if (++stage == S::kStages) stage = 0, phase ^= 1;
     };
-    while (w.next(p)) {
-      const Item& it = w.it;
+    // The two query rows of this lane's quad, loaded while the item before is joined.
+    uint32_t qf[4 * DC][4];
+    const auto load_queries = [&]() {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = w.it.row + g + 8 * i;
+        const int tok = div_of(row, p.group_div);
+        const bool real = g + 8 * i < w.it.rows;
+        const uint16_t* src = p.q + int64_t(w.it.req.first + tok) * p.q_stride +
+                              int64_t(w.head * p.group + (row - tok * p.group)) * D + 2 * c;
+#pragma unroll
+        for (int k = 0; k < 4 * DC; ++k) {
+          qf[k][i] = qf[k][2 + i] = 0;
+          if (real && 16 * k < D) {
+            qf[k][i] = *reinterpret_cast<const uint32_t*>(src + 16 * k);
+            qf[k][2 + i] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 8);
+          }
+        }
+      }
+    };
+    bool more = w.next(p);
+    if (more) load_queries();
+    while (more) {
+      const Item it = w.it;
+      const int head = w.head, piece = w.piece, first = w.first, last = w.last;
+      const bool whole = w.whole;
       const bool prefix = it.request < 0;
       const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
       const int tok0 = div_of(it.row, p.group_div);
       const int tok1 = div_of(it.row + it.rows - 1, p.group_div);
       const int pos0 = prefix ? it.req.row0 : it.req.row0 + tok0;
       const int pos1 = prefix ? it.req.row0 : it.req.row0 + tok1;
-      // The two query rows of this lane's quad and their positions.
-      uint32_t qf[4 * DC][4];
       int pos[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = it.row + g + 8 * i;
-        const int tok = div_of(row, p.group_div);
-        const bool real = g + 8 * i < it.rows;
-        pos[i] = row_position(p, it, row);
-        const uint16_t* src = p.q + int64_t(it.req.first + tok) * p.q_stride +
-                              int64_t(w.head * p.group + (row - tok * p.group)) * D + 2 * c;
+      for (int i = 0; i < 2; ++i) pos[i] = row_position(p, it, it.row + g + 8 * i);
+      if (p.q_flip != 0) {
 #pragma unroll
-        for (int k = 0; k < 4 * DC; ++k) {
-          uint32_t lo = 0, hi = 0;
-          if (real && 16 * k < D) {
-            lo = *reinterpret_cast<const uint32_t*>(src + 16 * k) ^ p.q_flip;
-            hi = *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) ^ p.q_flip;
-          }
-          qf[k][i] = lo;
-          qf[k][2 + i] = hi;
-        }
+        for (int k = 0; k < 4 * DC; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[k][i] ^= p.q_flip;
       }
       float acc[8 * DC][4];
 #pragma unroll
@@ -133,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
       float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};  // m in log2 units
 
-      for (int u = w.first; u < w.last; ++u, ++unit_count) {
+      for (int u = first; u < last; ++u, ++unit_count) {
         const int key0 = unit_key<kRowKeys>(it.span, u) + 16 * warp;
         const bool used = key0 < it.span.hi && (key0 + 16 > it.span.lo || key0 < it.span.sink_end);
         if (!(ok = mbar_wait(ring.full + 8 * stage, phase, ring.dead))) break;
@@ -153,12 +167,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           holes = (no_page[unit_count & 3][warp >> 1] >> (16 * (warp & 1))) & 0xFFFFu;
         }
         release();
-        bool mixed = false;
+        bool full = true, mixed = false;
+        uint32_t keep[2] = {~0u, ~0u};  // keys 2 c, 2 c + 1 and 8 on that some row sees
         uint32_t a[4] = {0, 0, 0, 0};
         if (used) {
           // s[t][e]: row e / 2, key 2 c + (e & 1) + 8 t of the sixteen
-          const bool full = holes == 0 && key0 + 15 <= pos0 &&
-                            (window == 0 || pos1 - key0 < window || key0 + 15 < sinks);
+          full = holes == 0 && key0 + 15 <= pos0 &&
+                 (window == 0 || pos1 - key0 < window || key0 + 15 < sinks);
+          if (!full) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              keep[h] = 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int j = 2 * c + e + 8 * h, key = key0 + j;
+                if (key < it.span.hi && (key >= it.span.lo || key < it.span.sink_end) &&
+                    !((holes >> j) & 1))
+                  keep[h] |= e ? 0xFFFF0000u : 0xFFFFu;
+              }
+            }
+          }
           float most[2] = {kNegInf, kNegInf};
 #pragma unroll
           for (int t = 0; t < 2; ++t)
@@ -215,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; 16 * k < D; ++k) {
               uint32_t b[4];
               ldmatrix4_t(b, tile + at(v_key, 2 * k + v_half));
-              bad |= T::not_finite(b[0]) | T::not_finite(b[1]) | T::not_finite(b[2]) |
-                     T::not_finite(b[3]);
+              bad |= T::not_finite(b[0] & keep[0]) | T::not_finite(b[1] & keep[1]) |
+                     T::not_finite(b[2] & keep[0]) | T::not_finite(b[3] & keep[1]);
             }
             bad = __any_sync(~0u, bad);
           }
@@ -226,16 +254,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (16 * k < D) {
                 uint32_t b[4];
                 ldmatrix4_t(b, tile + at(v_key, 2 * k + v_half));
+                if (!full) b[0] &= keep[0], b[1] &= keep[1], b[2] &= keep[0], b[3] &= keep[1];
                 T::mma(acc[2 * k], a, b[0], b[1]);
                 T::mma(acc[2 * k + 1], a, b[2], b[3]);
               }
           } else {
             for (int here = pos0; here <= pos1; ++here) {
-              uint32_t keep[2];
+              uint32_t seen[2];
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                keep[h] = (sees(key0 + 2 * c + 8 * h, here, window, sinks) ? 0xFFFFu : 0u) |
-                          (sees(key0 + 2 * c + 1 + 8 * h, here, window, sinks) ? 0xFFFF0000u : 0u);
+                seen[h] = keep[h] &
+                          ((sees(key0 + 2 * c + 8 * h, here, window, sinks) ? 0xFFFFu : 0u) |
+                           (sees(key0 + 2 * c + 1 + 8 * h, here, window, sinks) ? 0xFFFF0000u : 0u));
 #pragma unroll
               for (int k = 0; k < 4 * DC; ++k)
                 if (16 * k < D) {
@@ -244,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int h = 0; h < 2; ++h) {
                     float part[4] = {0.f, 0.f, 0.f, 0.f};
-                    T::mma(part, a, b[2 * h] & keep[0], b[2 * h + 1] & keep[1]);
+                    T::mma(part, a, b[2 * h] & seen[0], b[2 * h + 1] & seen[1]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                       if (pos[e >> 1] == here) acc[2 * k + h][e] += part[e];
@@ -255,6 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         release();
       }
+
+      more = w.next(p);
+      if (more) load_queries();
 
       // Join the warps: sums over the quad, then under the common maximum.
 #pragma unroll
@@ -305,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kWarps; ++k) ll += stat_l[k][row] * weight_of(stat_m[k][row], mm);
           const int tok = div_of(it.row + row, p.group_div);
           const int64_t t = it.req.first + tok;
-          const int qh = w.head * p.group + it.row + row - tok * p.group;
-          if (!w.whole) {
-            const int64_t to = int64_t(w.piece) * kRowTile + row;
+          const int qh = head * p.group + it.row + row - tok * p.group;
+          if (!whole) {
+            const int64_t to = int64_t(piece) * kRowTile + row;
             *reinterpret_cast<float4*>(p.rows.pieces + to * D + d) = o;
             if (d == 0) p.rows.stats[to] = make_float2(mm, ll);
           } else if (p.shared) {

@@ -3,10 +3,13 @@
 // Tiles of K and V take turns in a ring of stages.  A tile is [64-channel
 // block][key][64 channels] in the 128-byte swizzle (16-byte chunk index xor key
 // mod 8), as the tensor cores and ldmatrix both take it.  Two warps bring half
-// of a tile's keys each: by TMA where all of the half can be seen and lies in
-// runs of eight rows or more, else row by row (cp.async; a page may end
-// anywhere in a tile), with zeros for what no row of the item sees: a weight of
-// zero would not hide what lies there if it is not finite.
+// of a tile's keys each.  A weight of zero does not hide a value that is not
+// finite, so keys that no row of the item sees need care:
+//   load_kv     brings zeros for them: by TMA where all of the half can be seen
+//               and lies in runs of eight rows or more, else row by row
+//               (cp.async; a page may end anywhere in a tile)
+//   load_boxes  brings whole TMA boxes, for a reader that hides the rest by
+//               itself; what no row sees is there or is left from before
 #pragma once
 
 #include "attend.cuh"
@@ -152,6 +155,81 @@ __device__ __forceinline__ bool load_kv(const AttnParams& p, Walk<kTile, kKeys>&
   cp_async_wait<0>();
   if (tiles > 0) pass_on(1);
   return ok;
+}
+
+// The same by boxes alone (box > 0), without zeros.
+template <int DC, int kTile, int kKeys, int kStages>
+__device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKeys>& w,
+                                           const Ring& ring, const CUtensorMap* k_map,
+                                           const CUtensorMap* v_map, int box, int wk) {
+  constexpr int kBlock = kKeys * 128, kStage = DC * kBlock;
+  constexpr int kMine = kKeys / kLoadWarps;
+  static_assert(kMine / 8 * DC <= 32 && kMine <= 64, "a lane has at most one box");
+  const int lane = threadIdx.x & 31;
+  const int b = lane % DC, own = lane / DC * box;  // the lane's box: channels, first key
+  uint32_t stage = 0, phase = 1, unit_count = 0;
+  // One unit: where the lane's box lies; looked up while the unit before is issued.
+  struct Ahead {
+    int page, row_in_page, head;  // page -2: no row of the item sees the box
+    bool unit;
+  } next;
+  const int32_t* table = nullptr;
+  int u = 0;
+  w.last = 0;
+  const auto look_up = [&]() {
+    next.unit = true;
+    while (u >= w.last) {
+      if (!w.next(p)) {
+        next.unit = false;
+        return;
+      }
+      u = w.first;
+      table = w.it.request < 0 ? p.prefix_table : p.tables + int64_t(w.it.request) * p.max_pages;
+    }
+    const int key = unit_key<kKeys>(w.it.span, u) + kMine * wk + own;
+    next.page = -2;
+    next.head = w.head;
+    if (own < kMine && key < w.it.span.hi &&
+        (key + box > w.it.span.lo || key < w.it.span.sink_end)) {
+      const int col = div_of(key, p.page_div);
+      next.row_in_page = key - col * p.page_tokens;
+      next.page = max(-1, __ldg(table + col));
+    }
+    ++u;
+  };
+  look_up();
+  for (; next.unit; ++unit_count) {
+    const Ahead now = next;
+    look_up();
+    const bool hole = now.page == -1 || now.page >= p.num_pages;
+    const bool mine = now.page >= 0 && !hole;
+    const int row = mine ? now.page * p.page_tokens + now.row_in_page : 0;
+    const uint32_t bytes = __popc(__ballot_sync(~0u, mine)) * box * 128;
+    uint32_t holes[2] = {0, 0};
+    if (__any_sync(~0u, hole)) {
+      const uint64_t bits = hole ? (box < 64 ? (1ull << box) - 1 : ~0ull) << own : 0ull;
+      holes[0] = __reduce_or_sync(~0u, uint32_t(bits));
+      holes[1] = __reduce_or_sync(~0u, uint32_t(bits >> 32));
+      if (lane == 0) report(p.status, CG_ERR_MISMATCH);
+    }
+    for (int kv = 0; kv < 2; ++kv) {
+      if (!mbar_wait(ring.empty + 8 * stage, phase, ring.dead)) return false;
+      if (lane == 0) {
+        if (kv == 0) {
+#pragma unroll
+          for (int i = 0; i < kMine / 32; ++i)
+            ring.no_page[unit_count & 3][wk * (kMine / 32) + i] = holes[i];
+        }
+        mbar_expect(ring.full + 8 * stage, bytes);
+      }
+      __syncwarp();
+      if (mine)
+        tma_load3(ring.smem + stage * kStage + b * kBlock + (kMine * wk + own) * 128,
+                  kv ? v_map : k_map, 64 * b, now.head, row, ring.full + 8 * stage);
+      if (++stage == kStages) stage = 0, phase ^= 1;
+    }
+  }
+  return true;
 }
 
 }  // namespace cg
