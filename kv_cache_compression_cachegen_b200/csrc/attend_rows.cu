@@ -7,9 +7,14 @@
 // at most 16 query rows, so the bytes of K and V bound it, and all that counts
 // is that enough of them are on their way: one CTA an SM, whose ring of stages
 // (kv_loader.cuh) takes most of the shared memory, about 190 KB.  Eight warps
-// read the stages, 16 keys of each unit a warp, with the 16-row matrix
-// instructions of a warp (fewer rows than the tensor-memory products want);
-// each warp keeps a maximum, sums and outputs of its own, joined once an item.
+// read the stages, 16 keys of each unit a warp, with the matrix instructions of
+// a warp (the tensor-memory products want 128 rows).  The keys, and then the
+// channels, are the 16 rows of those, the query rows their 8 columns,
+//     S^T = K Q^T,   O^T = V^T P^T,
+// so that up to eight query rows take one product and not a half-empty larger
+// one: an m16n8k16 holds an SM's quarter for 32 cycles, and two products for
+// each would take longer than the bytes.  Each warp keeps a maximum, sums and
+// outputs of its own, joined once an item.
 #include <algorithm>
 
 #include "attend.cuh"
@@ -20,7 +25,7 @@ namespace {
 
 constexpr int kWarps = 8;  // that compute
 constexpr int kThreads = 32 * (kWarps + kLoadWarps);
-constexpr int kJoinBytes = 16 * 1024;
+constexpr int kJoinBytes = 17 * 1024;
 constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
 static_assert(kRowKeys == 16 * kWarps, "each warp takes 16 keys of a unit");
 static_assert(kJoinBytes >= (kScanSlots + 1) * 8, "the line's sums lie there at first");
@@ -29,9 +34,12 @@ template <int DC>
 struct Shape {
   static constexpr int kStages = DC == 4 ? 3 : (DC == 2 ? 6 : 8);
   static constexpr int kStage = DC * kRowKeys * 128;
-  static constexpr int kChannels = 64 * DC;
-  static constexpr int kJoinRows = std::min(16, kJoinBytes / (kWarps * kChannels * 4));
+  // a row of a warp's output for the join: four channels more, so that the four
+  // rows that a store touches fall on different banks
+  static constexpr int kPitch = 64 * DC + 4;
+  static constexpr int kJoinRows = kJoinBytes / (kWarps * kPitch * 4) >= 4 ? 4 : 2;
   static constexpr int kSmem = kStages * kStage + kJoinBytes + 1024;
+  static_assert(kJoinRows * kWarps * kPitch * 4 <= kJoinBytes, "");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -46,11 +54,18 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// The transpose of an 8 x 8 matrix of 16-bit values spread over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 __device__ __forceinline__ void compute_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 }
 
-template <typename T, int DC>
+// NR: products of eight query rows, 1 or 2.
+template <typename T, int DC, int NR>
 __global__ void __launch_bounds__(kThreads, 1)
     rows_kernel(AttnParams p, const __grid_constant__ KvMaps maps) {
   using S = Shape<DC>;
@@ -87,8 +102,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (any) {
     const int g = lane >> 2, c = lane & 3, D = p.dim;
     // this lane's part of an ldmatrix address: K tiles by key, V tiles transposed
-    const int k_key = 16 * warp + ((lane >> 4) << 3) + (lane & 7), k_half = (lane >> 3) & 1;
-    const int v_key = 16 * warp + (((lane >> 3) & 1) << 3) + (lane & 7), v_half = lane >> 4;
+    const int k_key = 16 * warp + (lane & 15), k_half = lane >> 4;
+    const int v_key = 16 * warp + ((lane >> 4) << 3) + (lane & 7), v_half = (lane >> 3) & 1;
     const auto at = [](int key, int chunk) {  // byte of a 16-byte chunk in a tile
       return uint32_t((chunk >> 3) * (kRowKeys * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4));
     };
@@ -99,22 +114,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(ring.empty + 8 * stage);
       if (++stage == S::kStages) stage = 0, phase ^= 1;
     };
-    // The two query rows of this lane's quad, loaded while the item before is joined.
-    uint32_t qf[4 * DC][4];
+    // Query row g (and g + 8), loaded while the item before is joined.
+    uint32_t qf[4 * DC][2 * NR];
     const auto load_queries = [&]() {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = w.it.row + g + 8 * i;
+      for (int n = 0; n < NR; ++n) {
+        const int row = w.it.row + g + 8 * n;
         const int tok = div_of(row, p.group_div);
-        const bool real = g + 8 * i < w.it.rows;
+        const bool real = g + 8 * n < w.it.rows;
         const uint16_t* src = p.q + int64_t(w.it.req.first + tok) * p.q_stride +
                               int64_t(w.head * p.group + (row - tok * p.group)) * D + 2 * c;
 #pragma unroll
         for (int k = 0; k < 4 * DC; ++k) {
-          qf[k][i] = qf[k][2 + i] = 0;
+          qf[k][2 * n] = qf[k][2 * n + 1] = 0;
           if (real && 16 * k < D) {
-            qf[k][i] = *reinterpret_cast<const uint32_t*>(src + 16 * k);
-            qf[k][2 + i] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 8);
+            qf[k][2 * n] = *reinterpret_cast<const uint32_t*>(src + 16 * k);
+            qf[k][2 * n + 1] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 8);
           }
         }
       }
@@ -131,49 +146,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok1 = div_of(it.row + it.rows - 1, p.group_div);
       const int pos0 = prefix ? it.req.row0 : it.req.row0 + tok0;
       const int pos1 = prefix ? it.req.row0 : it.req.row0 + tok1;
-      int pos[2];
+      // this lane's scores: keys g and g + 8, query rows 8 n + 2 c + e
+      int pos[NR][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) pos[i] = row_position(p, it, it.row + g + 8 * i);
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) pos[n][e] = row_position(p, it, it.row + 8 * n + 2 * c + e);
       if (p.q_flip != 0) {
 #pragma unroll
         for (int k = 0; k < 4 * DC; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qf[k][i] ^= p.q_flip;
+          for (int i = 0; i < 2 * NR; ++i) qf[k][i] ^= p.q_flip;
       }
-      float acc[8 * DC][4];
+      // channels 16 k + g and 8 on, of the same rows
+      float acc[4 * DC][NR][4];
 #pragma unroll
-      for (int j = 0; j < 8 * DC; ++j)
+      for (int k = 0; k < 4 * DC; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-      float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};  // m in log2 units
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[k][n][e] = 0.f;
+      float m[NR][2], l[NR][2];  // m in log2 units
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) m[n][e] = kNegInf, l[n][e] = 0.f;
 
       for (int u = first; u < last; ++u, ++unit_count) {
         const int key0 = unit_key<kRowKeys>(it.span, u) + 16 * warp;
         const bool used = key0 < it.span.hi && (key0 + 16 > it.span.lo || key0 < it.span.sink_end);
         if (!(ok = mbar_wait(ring.full + 8 * stage, phase, ring.dead))) break;
-        // S = Q K^T for 16 keys, as two tiles of 8
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float s[NR][4];
         uint32_t holes = 0;
         if (used) {
           const uint32_t tile = ring.smem + stage * S::kStage;
+          float half[2][NR][4];  // two chains of products
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) half[0][n][e] = half[1][n][e] = 0.f;
 #pragma unroll
           for (int k = 0; k < 4 * DC; ++k)
             if (16 * k < D) {
-              uint32_t b[4];
-              ldmatrix4(b, tile + at(k_key, 2 * k + k_half));
-              T::mma(s[0], qf[k], b[0], b[1]);
-              T::mma(s[1], qf[k], b[2], b[3]);
+              uint32_t a[4];
+              ldmatrix4(a, tile + at(k_key, 2 * k + k_half));
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                T::mma(half[k & 1][n], a, qf[k][2 * n], qf[k][2 * n + 1]);
             }
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = half[0][n][e] + half[1][n][e];
           holes = (no_page[unit_count & 3][warp >> 1] >> (16 * (warp & 1))) & 0xFFFFu;
         }
         release();
         bool full = true, mixed = false;
         uint32_t keep[2] = {~0u, ~0u};  // keys 2 c, 2 c + 1 and 8 on that some row sees
-        uint32_t a[4] = {0, 0, 0, 0};
+        uint32_t b[NR][2];
         if (used) {
-          // s[t][e]: row e / 2, key 2 c + (e & 1) + 8 t of the sixteen
           full = holes == 0 && key0 + 15 <= pos0 &&
                  (window == 0 || pos1 - key0 < window || key0 + 15 < sinks);
+          mixed = !full && tok0 != tok1;
           if (!full) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -187,49 +221,57 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          float most[2] = {kNegInf, kNegInf};
+          // s[n][e]: key g + 8 * (e >> 1), query row 8 n + 2 c + (e & 1)
+          float most[NR][2];
+          bool move = false;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int n = 0; n < NR; ++n) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              s[t][e] *= p.scale_log2;
+              s[n][e] *= p.scale_log2;
               if (!full) {
-                const int j = 2 * c + (e & 1) + 8 * t;
-                if (((holes >> j) & 1) || !sees(key0 + j, pos[e >> 1], window, sinks))
-                  s[t][e] = kNegInf;
+                const int j = g + 8 * (e >> 1);
+                if (((holes >> j) & 1) || !sees(key0 + j, pos[n][e & 1], window, sinks))
+                  s[n][e] = kNegInf;
               }
-              most[e >> 1] = fmaxf(most[e >> 1], s[t][e]);
             }
-          mixed = !full && tok0 != tok1;
-          // The maximum moves only when a score passes it by 2^8: weights up to
-          // that are in range of both types, and nothing is rescaled until then.
-          if (__any_sync(~0u, most[0] > m[0] + kSlack || most[1] > m[1] + kSlack)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              most[i] = fmaxf(most[i], __shfl_xor_sync(~0u, most[i], 1));
-              most[i] = fmaxf(most[i], __shfl_xor_sync(~0u, most[i], 2));
-              const float next = fmaxf(m[i], most[i]);
-              const float f = m[i] == next ? 1.f : exp2_fast(m[i] - next);
-              m[i] = next;
-              l[i] *= f;
-#pragma unroll
-              for (int j = 0; j < 8 * DC; ++j) acc[j][2 * i] *= f, acc[j][2 * i + 1] *= f;
+            for (int e = 0; e < 2; ++e) {
+              most[n][e] = fmaxf(s[n][e], s[n][2 + e]);
+              move |= most[n][e] > m[n][e] + kSlack;
             }
           }
-          float pr[2][4];
+          // The maximum moves only when a score passes it by 2^8: weights up to
+          // that are in range of both types, and nothing is rescaled until then.
+          if (__any_sync(~0u, move)) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1)
+                  most[n][e] = fmaxf(most[n][e], __shfl_xor_sync(~0u, most[n][e], x));
+                const float next = fmaxf(m[n][e], most[n][e]);
+                const float f = m[n][e] == next ? 1.f : exp2_fast(m[n][e] - next);
+                m[n][e] = next;
+                l[n][e] *= f;
+#pragma unroll
+                for (int k = 0; k < 4 * DC; ++k) acc[k][n][e] *= f, acc[k][n][2 + e] *= f;
+              }
+          }
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            float w8[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              pr[t][e] = s[t][e] == kNegInf ? 0.f : exp2_fast(s[t][e] - m[e >> 1]);
-              l[e >> 1] += pr[t][e];
+              w8[e] = s[n][e] == kNegInf ? 0.f : exp2_fast(s[n][e] - m[n][e & 1]);
+              l[n][e & 1] += w8[e];
             }
-          // Rounded to the pool's type for the product with V: half a step of it
-          // relative to each weight; the sum l is not.
-          a[0] = T::pack(pr[0][0], pr[0][1]);
-          a[1] = T::pack(pr[0][2], pr[0][3]);
-          a[2] = T::pack(pr[1][0], pr[1][1]);
-          a[3] = T::pack(pr[1][2], pr[1][3]);
+            // Rounded to the pool's type for the product with V: half a step of it
+            // relative to each weight; the sum l is not.
+            b[n][0] = transpose8(T::pack(w8[0], w8[1]));
+            b[n][1] = transpose8(T::pack(w8[2], w8[3]));
+          }
         }
         if (!(ok = mbar_wait(ring.full + 8 * stage, phase, ring.dead))) break;
         if (used) {
@@ -241,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (mixed) {
 #pragma unroll 1
             for (int k = 0; 16 * k < D; ++k) {
-              uint32_t b[4];
-              ldmatrix4_t(b, tile + at(v_key, 2 * k + v_half));
-              bad |= T::not_finite(b[0] & keep[0]) | T::not_finite(b[1] & keep[1]) |
-                     T::not_finite(b[2] & keep[0]) | T::not_finite(b[3] & keep[1]);
+              uint32_t a[4];
+              ldmatrix4_t(a, tile + at(v_key, 2 * k + v_half));
+              bad |= T::not_finite(a[0] & keep[0]) | T::not_finite(a[1] & keep[0]) |
+                     T::not_finite(a[2] & keep[1]) | T::not_finite(a[3] & keep[1]);
             }
             bad = __any_sync(~0u, bad);
           }
@@ -252,11 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4 * DC; ++k)
               if (16 * k < D) {
-                uint32_t b[4];
-                ldmatrix4_t(b, tile + at(v_key, 2 * k + v_half));
-                if (!full) b[0] &= keep[0], b[1] &= keep[1], b[2] &= keep[0], b[3] &= keep[1];
-                T::mma(acc[2 * k], a, b[0], b[1]);
-                T::mma(acc[2 * k + 1], a, b[2], b[3]);
+                uint32_t a[4];
+                ldmatrix4_t(a, tile + at(v_key, 2 * k + v_half));
+                if (!full) a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
+#pragma unroll
+                for (int n = 0; n < NR; ++n) T::mma(acc[k][n], a, b[n][0], b[n][1]);
               }
           } else {
             for (int here = pos0; here <= pos1; ++here) {
@@ -269,15 +311,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4 * DC; ++k)
                 if (16 * k < D) {
-                  uint32_t b[4];
-                  ldmatrix4_t(b, tile + at(v_key, 2 * k + v_half));
+                  uint32_t a[4];
+                  ldmatrix4_t(a, tile + at(v_key, 2 * k + v_half));
+                  a[0] &= seen[0], a[1] &= seen[0], a[2] &= seen[1], a[3] &= seen[1];
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
+                  for (int n = 0; n < NR; ++n) {
                     float part[4] = {0.f, 0.f, 0.f, 0.f};
-                    T::mma(part, a, b[2 * h] & seen[0], b[2 * h + 1] & seen[1]);
+                    T::mma(part, a, b[n][0], b[n][1]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                      if (pos[e >> 1] == here) acc[2 * k + h][e] += part[e];
+                      if (pos[n][e & 1] == here) acc[k][n][e] += part[e];
                   }
                 }
             }
@@ -289,37 +332,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       more = w.next(p);
       if (more) load_queries();
 
-      // Join the warps: sums over the quad, then under the common maximum.
+      // Join the warps: sums over the lanes of a row, then under the common maximum.
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(~0u, l[i], 1);
-        l[i] += __shfl_xor_sync(~0u, l[i], 2);
-        if (c == 0) {
-          stat_m[warp][g + 8 * i] = m[i];
-          stat_l[warp][g + 8 * i] = l[i];
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], x);
+          if (g == 0) {
+            stat_m[warp][8 * n + 2 * c + e] = m[n][e];
+            stat_l[warp][8 * n + 2 * c + e] = l[n][e];
+          }
         }
-      }
       compute_sync();
-      float f[2];
+      float f[NR][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float top = kNegInf;
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, stat_m[k][g + 8 * i]);
-        f[i] = weight_of(m[i], top);
-      }
+        for (int e = 0; e < 2; ++e) {
+          float top = kNegInf;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) top = fmaxf(top, stat_m[k][8 * n + 2 * c + e]);
+          f[n][e] = weight_of(m[n][e], top);
+        }
       const int quads = D / 4;
       for (int r0 = 0; r0 < it.rows; r0 += S::kJoinRows) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = g + 8 * i - r0;
-          if (row < 0 || row >= S::kJoinRows) continue;
-          float* dst = join + (warp * S::kJoinRows + row) * S::kChannels + 2 * c;
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int j = 0; j < 8 * DC; ++j)
-            *reinterpret_cast<float2*>(dst + 8 * j) =
-                make_float2(acc[j][2 * i] * f[i], acc[j][2 * i + 1] * f[i]);
-        }
+          for (int e = 0; e < 2; ++e) {
+            const int row = 8 * n + 2 * c + e - r0;
+            if (row < 0 || row >= S::kJoinRows) continue;
+            float* dst = join + (warp * S::kJoinRows + row) * S::kPitch + g;
+#pragma unroll
+            for (int k = 0; k < 4 * DC; ++k) {
+              dst[16 * k] = acc[k][n][e] * f[n][e];
+              dst[16 * k + 8] = acc[k][n][2 + e] * f[n][e];
+            }
+          }
         compute_sync();
         // thread: four channels of a row
         const int rows = min(S::kJoinRows, it.rows - r0);
@@ -330,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kWarps; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(
-                join + (k * S::kJoinRows + r) * S::kChannels + d);
+                join + (k * S::kJoinRows + r) * S::kPitch + d);
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
             mm = fmaxf(mm, stat_m[k][row]);
           }
@@ -366,21 +416,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_previous();
 }
 
-template <typename T, int DC>
+template <typename T, int DC, int NR>
 cudaError_t launch(const AttnParams& p, bool early, cudaStream_t stream) {
   using S = Shape<DC>;
   const cudaError_t err = cudaFuncSetAttribute(
-      rows_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+      rows_kernel<T, DC, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (err != cudaSuccess) return err;
-  return launch_after(rows_kernel<T, DC>, p.rows.ctas, kThreads, S::kSmem, stream, early, p,
+  return launch_after(rows_kernel<T, DC, NR>, p.rows.ctas, kThreads, S::kSmem, stream, early, p,
                       kv_maps(p, kRowKeys / kLoadWarps, T::kBf16));
+}
+
+template <typename T, int DC>
+cudaError_t launch_dim(const AttnParams& p, bool early, cudaStream_t stream) {
+  // can an item have more than eight rows?
+  const int64_t most = int64_t(p.prefix_small ? p.num_tokens : p.max_q) * p.group;
+  return most > 8 ? launch<T, DC, 2>(p, early, stream) : launch<T, DC, 1>(p, early, stream);
 }
 
 template <typename T>
 cudaError_t launch_type(const AttnParams& p, bool early, cudaStream_t stream) {
-  if (p.dim <= 64) return launch<T, 1>(p, early, stream);
-  if (p.dim <= 128) return launch<T, 2>(p, early, stream);
-  return launch<T, 4>(p, early, stream);
+  if (p.dim <= 64) return launch_dim<T, 1>(p, early, stream);
+  if (p.dim <= 128) return launch_dim<T, 2>(p, early, stream);
+  return launch_dim<T, 4>(p, early, stream);
 }
 
 }  // namespace
