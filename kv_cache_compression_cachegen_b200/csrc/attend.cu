@@ -24,113 +24,105 @@ struct Part {
   const Lane* lane;
 
   __device__ __forceinline__ int count() const { return c1 - c0 + 1; }
-  __device__ __forceinline__ int64_t at(int i) const {
-    // an item begins in its first CTA's share and is at the head of the others'
-    return int64_t(2 * (c0 + i) + (i == 0 ? 1 : 0)) * lane->tile + in_tile;
-  }
-  __device__ __forceinline__ float2 stat(const AttnParams& p, int i) const {
-    return c0 == c1 ? p.whole_stats[whole_at] : lane->stats[at(i)];
-  }
-  __device__ __forceinline__ const float* values(const AttnParams& p, int i) const {
-    return c0 == c1 ? p.whole + whole_at * p.dim : lane->pieces + at(i) * p.dim;
+  __device__ __forceinline__ void at(const AttnParams& p, int i, const float2*& stat,
+                                     const float*& values) const {
+    if (c0 == c1) {
+      stat = p.whole_stats + whole_at;
+      values = p.whole + whole_at * p.dim;
+    } else {
+      // an item begins in its first CTA's share and is at the head of the others'
+      const int64_t k = int64_t(2 * (c0 + i) + (i == 0 ? 1 : 0)) * lane->tile + in_tile;
+      stat = lane->stats + k;
+      values = lane->pieces + k * p.dim;
+    }
   }
 };
 
-// One warp joins one (token, query head) row: the lanes first look at the
-// parts' maxima, then add up the parts, a lane four channels of each.
-template <typename T, int kParts>
+constexpr int kJoinThreads = 256;
+constexpr int kRowLanes = 8;  // threads of a row
+constexpr int kJoinRows = kJoinThreads / kRowLanes;
+
+// Eight threads join one (token, query head) row, each kQuads times four
+// channels.  Four parts at a time are asked for together, their maxima and
+// sums with their values: most rows have no more, and wait once.
+template <typename T, int kQuads, int kParts>
 __device__ __forceinline__ void join_row(const AttnParams& p, const Part (&part)[kParts], int t,
                                          int qh) {
-  const int lane = threadIdx.x & 31, D = p.dim;
+  const int lane = threadIdx.x % kRowLanes, D = p.dim;
   const int n0 = part[0].count(), n = n0 + (kParts > 1 ? part[kParts - 1].count() : 0);
-  const auto of = [&](int i) -> const Part& { return kParts > 1 && i >= n0 ? part[kParts - 1] : part[0]; };
-  float mm = kNegInf;
-  for (int i = lane; i < n; i += 32) mm = fmaxf(mm, of(i).stat(p, i < n0 ? i : i - n0).x);
+  float mm = kNegInf, ll = 0.f;
+  float4 o[kQuads];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-  float ll = 0.f;
-  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int mine = i0 + lane, have = min(32, n - i0);
-    float f = 0.f;
-    if (mine < n) {
-      const float2 st = of(mine).stat(p, mine < n0 ? mine : mine - n0);
-      f = weight_of(st.x, mm);
-      ll += st.y * f;
+  for (int q = 0; q < kQuads; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 4) {
+    float2 st[4];
+    float4 v[4][kQuads];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      st[i] = make_float2(kNegInf, 0.f);
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) v[i][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i < n) {
+        const float2* stat;
+        const float* values;
+        if (kParts > 1 && i0 + i >= n0) part[kParts - 1].at(p, i0 + i - n0, stat, values);
+        else part[0].at(p, i0 + i, stat, values);
+        st[i] = *stat;
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+          if (4 * (q * kRowLanes + lane) < D)
+            v[i][q] = *reinterpret_cast<const float4*>(values + 4 * (q * kRowLanes + lane));
+      }
     }
-#pragma unroll 8
-    for (int i = 0; i < have; ++i) {
-      const int k = i0 + i;
-      const float fk = __shfl_sync(~0u, f, i);
-      const float* src = of(k).values(p, k < n0 ? k : k - n0) + 4 * lane;
+    float top = mm;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (128 * h + 4 * lane < D) {
-          const float4 v = *reinterpret_cast<const float4*>(src + 128 * h);
-          o[h].x += v.x * fk, o[h].y += v.y * fk, o[h].z += v.z * fk, o[h].w += v.w * fk;
-        }
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, st[i].x);
+    const float f0 = weight_of(mm, top);
+    mm = top;
+    ll *= f0;
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) o[q].x *= f0, o[q].y *= f0, o[q].z *= f0, o[q].w *= f0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = weight_of(st[i].x, top);
+      ll += st[i].y * f;
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        o[q].x += v[i][q].x * f, o[q].y += v[i][q].y * f;
+        o[q].z += v[i][q].z * f, o[q].w += v[i][q].w * f;
+      }
     }
   }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) ll += __shfl_xor_sync(~0u, ll, x);
   const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  uint16_t* out = p.out + int64_t(t) * p.out_stride + int64_t(qh) * D;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (128 * h + 4 * lane < D)
-      *reinterpret_cast<uint2*>(p.out + int64_t(t) * p.out_stride + int64_t(qh) * D + 128 * h +
-                                4 * lane) =
-          make_uint2(T::pack(o[h].x * inv, o[h].y * inv), T::pack(o[h].z * inv, o[h].w * inv));
+  for (int q = 0; q < kQuads; ++q)
+    if (4 * (q * kRowLanes + lane) < D)
+      *reinterpret_cast<uint2*>(out + 4 * (q * kRowLanes + lane)) =
+          make_uint2(T::pack(o[q].x * inv, o[q].y * inv), T::pack(o[q].z * inv, o[q].w * inv));
   if (lane == 0 && p.lse != nullptr) p.lse[int64_t(t) * p.q_heads + qh] = log_sum(mm, ll);
 }
 
-constexpr int kJoinWarps = 8;
-
-// Without a prefix only items that were cut are joined.  A line with c shares
-// has c - 1 cuts; the warps of a cut take the rows of the item that it goes
-// through, if it is the item's first cut.
-template <typename T, int kTile, int kKeys>
-__device__ __forceinline__ void join_cut(const AttnParams& p, const Lane& line, int cut, int first,
-                                         int step) {
-  const int slots = total_slots<kTile>(p), H = p.kv_heads;
-  const int64_t units = line.cum[slots] * H;
-  const int ctas = shares_of(line, units);
-  if (cut >= ctas) return;
-  const int64_t u = share_of(cut, units, ctas);
-  const int x = slot_of(line.cum, slots, H, u);
-  const int64_t cum = line.cum[x], cost = line.cum[x + 1] - cum;
-  const int head = int(uint32_t(u - cum * H) / uint32_t(cost));
-  const int64_t item0 = cum * H + head * cost;
-  if (item0 == u) return;  // between two items
-  Part part[1];
-  part[0].lane = &line;
-  part[0].c0 = cta_of(item0, units, ctas);
-  if (part[0].c0 != cut - 1) return;
-  part[0].c1 = cta_of(item0 + cost - 1, units, ctas);
-  Item it;
-  if (slot_item<kTile, kKeys>(p, x, it) == 0) return;
-  for (int r = first; r < it.rows; r += step) {
-    const int row = it.row + r, tok = div_of(row, p.group_div);
-    part[0].in_tile = r;
-    join_row<T>(p, part, it.req.first + tok, head * p.group + row - tok * p.group);
-  }
-}
-
-template <typename T, int kTile, int kKeys>
-__global__ void __launch_bounds__(32 * kJoinWarps) cuts_kernel(AttnParams p) {
+// Without a prefix only items that were cut are joined, each at its first cut,
+// which the CTA behind it has noted.
+template <typename T, int kTile>
+__global__ void __launch_bounds__(kJoinThreads) cuts_kernel(AttnParams p) {
   wait_for_previous();
-  const int warp = threadIdx.x >> 5;
-  constexpr int kRowBlocks = kRowTile / kJoinWarps;  // blocks of a cut of the rows kernel's line
-  constexpr int kTileBlocks = 8;
-  const int rows_first = kRowBlocks * (p.rows.ctas - 1);
-  int b = blockIdx.x;
-  if (b < rows_first) {
-    join_cut<T, kRowTile, kRowKeys>(p, p.rows, 1 + b / kRowBlocks,
-                                    b % kRowBlocks * kJoinWarps + warp, kRowTile);
+  constexpr int kBlocks = kTile / kJoinRows;  // blocks of a cut of the tile kernel's line
+  int b = int(blockIdx.x) - p.rows.ctas, r = threadIdx.x / kRowLanes;
+  const Lane& line = b < 0 ? p.rows : p.tiles;
+  if (b < 0) {
+    b += p.rows.ctas;
   } else {
-    b -= rows_first;
-    join_cut<T, kTile, kKeys>(p, p.tiles, 1 + b / kTileBlocks, b % kTileBlocks * kJoinWarps + warp,
-                              kTileBlocks * kJoinWarps);
+    r += b % kBlocks * kJoinRows;
+    b /= kBlocks;
   }
+  const Cut cut = line.cuts[b];
+  if (cut.c1 < cut.c0 || r >= cut.rows) return;
+  const int row = cut.row + r, tok = div_of(row, p.group_div);
+  const Part part[1] = {Part{cut.c0, cut.c1, r, 0, &line}};
+  join_row<T, kTile == 256 ? 4 : 8>(p, part, cut.first + tok,
+                                    cut.head * p.group + row - tok * p.group);
 }
 
 // With a prefix every row has two items, its own and the prefix's.
@@ -142,23 +134,28 @@ __device__ __forceinline__ Part find_part(const AttnParams& p, const Lane& line,
   part.whole_at = whole_at;
   const int x = (prefix ? own_slots<kTile>(p) : slot_base<kTile>(p, request)) + row / kTile;
   part.in_tile = row % kTile;
-  const int64_t cost = line.cum[x + 1] - line.cum[x];
+  const int64_t cum = line.cum[x], cost = line.cum[x + 1] - cum;
   const int64_t units = line.cum[total_slots<kTile>(p)] * p.kv_heads;
   const int ctas = shares_of(line, units);
-  const int64_t item0 = line.cum[x] * p.kv_heads + head * cost;
+  const int64_t item0 = cum * p.kv_heads + head * cost;
   part.c0 = cta_of(item0, units, ctas);
   part.c1 = cta_of(item0 + cost - 1, units, ctas);
   return part;
 }
 
 template <typename T, int kTile>
-__global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(AttnParams p) {
   wait_for_previous();
-  const int row_id = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int row_id = blockIdx.x * kJoinRows + threadIdx.x / kRowLanes;
   if (row_id >= p.num_tokens * p.q_heads) return;
   const int t = row_id / p.q_heads, qh = row_id - t * p.q_heads;
   if (t >= p.q_starts[p.num_requests]) return;
-  const int lo = request_of(p, t);
+  int lo = 0, hi = p.num_requests - 1;  // the last request that starts at or before t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.q_starts[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
   Request req;
   if (!load_request(p, lo, req) || t < req.first || t >= req.first + req.tokens) return;
   const int head = div_of(qh, p.group_div), member = qh - head * p.group;
@@ -170,14 +167,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(AttnParams
           : find_part<kTile>(p, p.tiles, false, lo, own, head, row_id),
       p.prefix_small ? find_part<kRowTile>(p, p.rows, true, lo, of_all, head, rows + row_id)
                      : find_part<kTile>(p, p.tiles, true, lo, of_all, head, rows + row_id)};
-  join_row<T>(p, part, t, qh);
+  join_row<T, kTile == 256 ? 4 : 8>(p, part, t, qh);
 }
 
 uint64_t up256(uint64_t v) { return (v + 255) & ~uint64_t(255); }
 
 struct Workspace {
-  uint64_t row_cum, row_pieces, row_stats, tile_cum, tile_pieces, tile_stats, whole, whole_stats,
-      total;
+  uint64_t row_cum, row_cuts, row_pieces, row_stats, tile_cum, tile_cuts, tile_pieces, tile_stats,
+      whole, whole_stats, total;
 };
 
 Workspace workspace_of(const cg_shape& s, int Hq, int tokens, int requests, bool shared) {
@@ -196,9 +193,11 @@ Workspace workspace_of(const cg_shape& s, int Hq, int tokens, int requests, bool
     return here;
   };
   w.row_cum = take((row_slots + 1) * 8);
+  w.row_cuts = take(kMaxCtas * sizeof(Cut));
   w.row_pieces = take(uint64_t(2) * kMaxCtas * kRowTile * D * 4);
   w.row_stats = take(uint64_t(2) * kMaxCtas * kRowTile * 8);
   w.tile_cum = take((tile_slots + 1) * 8);
+  w.tile_cuts = take(tile_ctas * sizeof(Cut));
   w.tile_pieces = take(2 * tile_ctas * tile * D * 4);
   w.tile_stats = take(2 * tile_ctas * tile * 8);
   w.whole = take(rows * D * 4);
@@ -227,12 +226,11 @@ cudaError_t launch_all(AttnParams& p, int sms, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   if (p.shared) {
     const int64_t all = int64_t(p.num_tokens) * p.q_heads;
-    return launch_after(shared_join_kernel<T, kTile>,
-                        unsigned((all + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, stream,
-                        true, p);
+    return launch_after(shared_join_kernel<T, kTile>, unsigned((all + kJoinRows - 1) / kJoinRows),
+                        kJoinThreads, 0, stream, true, p);
   }
-  const unsigned blocks = kRowTile / kJoinWarps * (p.rows.ctas - 1) + 8 * std::max(0, p.tiles.ctas - 1);
-  return launch_after(cuts_kernel<T, kTile, kKeys>, std::max(1u, blocks), 32 * kJoinWarps, 0,
+  return launch_after(cuts_kernel<T, kTile>,
+                      unsigned(p.rows.ctas + kTile / kJoinRows * p.tiles.ctas), kJoinThreads, 0,
                       stream, true, p);
 }
 
@@ -296,9 +294,11 @@ cudaError_t launch_attention(const cg_attention_args& a, const cg_shape& s,
   uint8_t* w = static_cast<uint8_t*>(a.workspace_dev);
   const Workspace ws = workspace_of(s, a.num_q_heads, a.num_tokens, a.num_requests, shared);
   p.rows.cum = reinterpret_cast<int64_t*>(w + ws.row_cum);
+  p.rows.cuts = reinterpret_cast<Cut*>(w + ws.row_cuts);
   p.rows.pieces = reinterpret_cast<float*>(w + ws.row_pieces);
   p.rows.stats = reinterpret_cast<float2*>(w + ws.row_stats);
   p.tiles.cum = reinterpret_cast<int64_t*>(w + ws.tile_cum);
+  p.tiles.cuts = reinterpret_cast<Cut*>(w + ws.tile_cuts);
   p.tiles.pieces = reinterpret_cast<float*>(w + ws.tile_pieces);
   p.tiles.stats = reinterpret_cast<float2*>(w + ws.tile_stats);
   p.whole = reinterpret_cast<float*>(w + ws.whole);

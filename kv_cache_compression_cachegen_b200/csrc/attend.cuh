@@ -32,8 +32,14 @@ constexpr int kRowKeys = 128;  // keys of a unit there
 constexpr int kScanSlots = 1024;  // slots of a line that every CTA sums up by itself
 
 // The line of work of one of the two kernels, in the workspace.
+struct Cut {
+  int first, row, rows;  // first packed row of q, first row of the tile, rows in it
+  int head, c0, c1;      // kv head, CTAs that have pieces; c1 < c0: nothing was cut here
+};
+
 struct Lane {
   int64_t* cum;   // [slots + 1] units of one head before each slot
+  Cut* cuts;      // [ctas] by each CTA: the item that its share begins in the middle of
   float* pieces;  // [2 * ctas][tile][dim] unnormalised outputs of cut items
   float2* stats;  // [2 * ctas][tile] (maximum in log2 units, sum)
   int ctas;       // CTAs of the kernel's grid, 0: not launched
@@ -302,11 +308,12 @@ __device__ __forceinline__ int slot_of(const int64_t* cum, int slots, int heads,
 // One CTA's share of a line, item by item.
 template <int kTile, int kKeys>
 struct Walk {
-  int64_t u, u_end, share0, cum;
-  int x, slots;
+  int64_t u, u_end, share0, cum, units;
+  int x, slots, ctas;
   // the current part: units [first, last) of an item of `cost` units at `head`
   Item it;
-  int head, first, last, piece;
+  int64_t item0;  // its first unit
+  int cost, head, first, last, piece;
   bool whole;
 
   // All threads of the block; cum_s has room for kScanSlots + 1.
@@ -319,8 +326,9 @@ struct Walk {
       if (blockIdx.x == 0)  // for the join
         for (int i = threadIdx.x; i <= slots; i += blockDim.x) lane.cum[i] = cum_s[i];
     }
-    const int64_t units = line[slots] * p.kv_heads;
-    const int ctas = shares_of(lane, units);
+    units = line[slots] * p.kv_heads;
+    ctas = shares_of(lane, units);
+    item0 = share0 = 0;
     if (int(blockIdx.x) >= ctas) return false;
     u = share_of(blockIdx.x, units, ctas);
     u_end = share_of(blockIdx.x + 1, units, ctas);
@@ -332,14 +340,14 @@ struct Walk {
 
   __device__ __forceinline__ bool next(const AttnParams& p) {
     while (u < u_end && x < slots) {
-      const int cost = slot_item<kTile, kKeys>(p, x, it);
+      cost = slot_item<kTile, kKeys>(p, x, it);
       if (cost == 0 || u >= (cum + cost) * p.kv_heads) {
         cum += cost;
         ++x;
         continue;
       }
       head = int(uint32_t(u - cum * p.kv_heads) / uint32_t(cost));  // a slot's units fit 31 bits
-      const int64_t item0 = cum * p.kv_heads + int64_t(head) * cost;
+      item0 = cum * p.kv_heads + int64_t(head) * cost;
       const int from = int(u - item0);
       const int to = int((item0 + cost < u_end ? item0 + cost : u_end) - item0);
       whole = from == 0 && to == cost;
@@ -351,6 +359,16 @@ struct Walk {
       return true;
     }
     return false;
+  }
+
+  // One thread, after the first next() (or none): what the join has to know.
+  __device__ __forceinline__ void note_cut(const Lane& lane, bool any) const {
+    Cut cut{0, 0, 0, 0, 0, -1};
+    // an item over several shares is joined at its first cut
+    if (any && item0 < share0 && cta_of(item0, units, ctas) + 1 == int(blockIdx.x))
+      cut = Cut{it.req.first, it.row, it.rows, head, int(blockIdx.x) - 1,
+                cta_of(item0 + cost - 1, units, ctas)};
+    lane.cuts[blockIdx.x] = cut;
   }
 };
 

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool any = w.begin(p, p.rows, reinterpret_cast<int64_t*>(join));
   __syncthreads();
 
+  if (!any && threadIdx.x == 0) w.note_cut(p.rows, false);
   if (any && warp >= kWarps) {
     if (maps.box > 0)
       load_boxes<DC, kRowTile, kRowKeys, S::kStages>(p, w, ring, &maps.k, &maps.v, maps.box,
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool more = w.next(p);
     if (more) load_queries();
+    if (threadIdx.x == 0) w.note_cut(p.rows, more);
     while (more) {
       const Item it = w.it;
       const int head = w.head, piece = w.piece, first = w.first, last = w.last;

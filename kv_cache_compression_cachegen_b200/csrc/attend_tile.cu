@@ -386,9 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kQueryWarp) {
       // ---- queries
       uint32_t q_phase = 3;  // a bit for each query tile
-      bool ok = any;
+      bool ok = any, noted = false;
+      if (!any && lane == 0) w.note_cut(p.tiles, false);
       while (ok && w.next(p)) {
         const Item& it = w.it;
+        if (!noted && lane == 0) w.note_cut(p.tiles, true);
+        noted = true;
         if (w.first >= w.last) continue;
         for (int tile = 0; tile < (it.rows > 128 ? 2 : 1); ++tile) {
           if (!(ok = mbar_wait(bar.q_free + 8 * tile, (q_phase >> tile) & 1, dead))) break;
