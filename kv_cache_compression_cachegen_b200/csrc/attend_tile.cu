@@ -6,8 +6,8 @@
 //                    thread): scores out of tensor memory, running maximum and
 //                    sum, weights back into tensor memory; output of the item
 //   warps 10, 11     K and V from the pages to shared memory (kv_loader.cuh)
-//   warp 9           queries to shared memory, as soon as the last product with
-//                    the item's before has read them
+//   warp 9           deals the items; queries to shared memory, as soon as the
+//                    last product with the item's before has read them
 //   warp 8           one thread issues the products:
 //                      S = Q K^T   both operands in shared memory
 //                      O += P V    P in tensor memory, V along its channels
@@ -52,6 +52,18 @@ struct Geometry {
 
 struct Bars {
   uint32_t q_full, q_free, s_full, p_full, o_full;  // each the first of its two
+  uint32_t item_full, item_free;                    // of kItems
+};
+
+// One part of an item, as the query warp deals it to the softmax warps and the
+// products; those have no registers to spare for the walk over the line.
+constexpr int kItems = 4;
+struct Deal {
+  int first, last;             // units
+  int sink_units, first_unit;  // of its span
+  int rows, row;               // 0 rows: the share is done
+  int token0, row0, request;   // first packed row of the request, its position, its number or -1
+  int head, piece, whole;
 };
 
 // 2^x of two values without the special-function unit, which alone would take
@@ -86,22 +98,22 @@ __device__ __forceinline__ uint32_t below(int n) {
 // the definition: a masked key's weight of zero does not hide an infinity or a
 // NaN in the matrix product.  o: four channels a lane and 128 channels apart.
 template <typename T>
-__device__ __forceinline__ void recompute_row(const AttnParams& p, const Item& it, int head, int row, int kKeys,
-                              int first, int last, float (&o)[2][4], float& m, float& l) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void recompute_row(const AttnParams& p, const Deal& it, int row,
+                                              int kKeys, float (&o)[2][4], float& m, float& l) {
+  const int lane = threadIdx.x & 31, head = it.head;
   const bool prefix = it.request < 0;
   const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
   const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
-  const int tok = div_of(row, p.group_div), at = row_position(p, it, row);
-  const uint16_t* q = p.q + int64_t(it.req.first + tok) * p.q_stride +
+  const int tok = div_of(row, p.group_div), at = prefix ? it.row0 : it.row0 + tok;
+  const uint16_t* q = p.q + int64_t(it.token0 + tok) * p.q_stride +
                       int64_t(head * p.group + row - tok * p.group) * p.dim;
   const int64_t step = int64_t(p.kv_heads) * p.dim;
   m = kNegInf;
   l = 0.f;
   for (int h = 0; h < 2; ++h)
     for (int e = 0; e < 4; ++e) o[h][e] = 0.f;
-  for (int u = first; u < last; ++u) {
-    const int unit = u < it.span.sink_units ? u : it.span.first_unit + u - it.span.sink_units;
+  for (int u = it.first; u < it.last; ++u) {
+    const int unit = u < it.sink_units ? u : it.first_unit + u - it.sink_units;
     for (int k0 = 0; k0 < kKeys; k0 += 32) {
       const int key = unit * kKeys + k0 + lane;
       int from = -1;
@@ -152,10 +164,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap q_map, int by_map) {
   using G = Geometry<DC>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars_mem[2 * G::kStages + 10];
+  __shared__ uint64_t bars_mem[2 * G::kStages + 10 + 2 * kItems];
+  __shared__ Deal deals[kItems];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_mem;
-  __shared__ uint32_t no_page[4][4];
+  __shared__ __align__(16) uint32_t no_page[4][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t q_smem = base;
@@ -169,6 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   bar.s_full = bar.q_free + 16;
   bar.p_full = bar.s_full + 16;
   bar.o_full = bar.p_full + 16;
+  bar.item_full = bar.o_full + 16;
+  bar.item_free = bar.item_full + 8 * kItems;
 
   let_next_start();
   if (threadIdx.x == 0) {
@@ -183,6 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar.s_full + 8 * i, 1);
       mbar_init(bar.p_full + 8 * i, 4);
       mbar_init(bar.o_full + 8 * i, 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bar.item_full + 8 * i, 1);
+      mbar_init(bar.item_free + 8 * i, 4 * G::kTiles + 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -204,62 +223,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = tmem + lanes + G::kO + tile * G::kOStep;
     uint32_t s_phase = 0, o_phase = 0, unit_count = 0;
     bool ok = any && tile < G::kTiles;
-    while (ok && w.next(p)) {
-      const Item& it = w.it;
-      const uint32_t before = unit_count;
-      unit_count += w.last - w.first;
-      if (it.rows <= 128 * tile) continue;  // no rows in this tile
+    for (uint32_t n = 0; ok; ++n) {
+      const Deal& it = deals[n % kItems];
+      if (!(ok = mbar_wait(bar.item_full + 8 * (n % kItems), (n / kItems) & 1, dead))) break;
+      if (it.rows == 0) break;
+      const int first = it.first, last = it.last;
+      if (it.rows <= 128 * tile) {  // no rows in this tile
+        unit_count += last - first;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.item_free + 8 * (n % kItems));
+        continue;
+      }
       const bool real = 128 * tile + r < it.rows;
-      const int row = it.row + (real ? 128 * tile + r : it.rows - 1);
-      const int tok = div_of(row, p.group_div);
-      const int64_t t = it.req.first + tok;
-      const int qh = w.head * p.group + row - tok * p.group;
       const bool prefix = it.request < 0;
-      const int pos = row_position(p, it, row);
+      const int row = it.row + (real ? 128 * tile + r : it.rows - 1);
+      const int pos = prefix ? it.row0 : it.row0 + div_of(row, p.group_div);
       const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
       float m = kNegInf, l = 0.f;
       bool mixed = false;  // some unit had keys that a row does not see
-      for (int u = w.first; u < w.last; ++u) {
+      for (int u = first; u < last; ++u, ++unit_count) {
         if (!(ok = mbar_wait(bar.s_full + 8 * tile, s_phase, dead))) break;
         s_phase ^= 1;
         tc_fence_after();
         uint32_t raw[G::kKeys];
 #pragma unroll
         for (int j = 0; j < G::kKeys; j += 64) tmem_load64(t_s + j, raw + j);
-        const int key0 = unit_key<G::kKeys>(it.span, u);
+        const int key0 =
+            (u < it.sink_units ? u : it.first_unit + u - it.sink_units) * G::kKeys;
         // the whole unit is seen by the row, or its keys are hidden one by one
         const int end = key0 + G::kKeys - 1;
-        const uint32_t* hole = no_page[(before + u - w.first) & 3];
-        uint32_t holes = 0;
-#pragma unroll
-        for (int i = 0; i < G::kKeys / 32; ++i) holes |= hole[i];
+        const uint4 hole = *reinterpret_cast<const uint4*>(no_page[unit_count & 3]);
         const bool full = end <= pos && (window == 0 || pos - key0 < window || end < sinks);
-        if (!__all_sync(~0u, full && holes == 0)) {
+        if (!__all_sync(~0u, full && (hole.x | hole.y | hole.z | hole.w) == 0)) {
           mixed = true;
           // keys before `past` are behind the window
           const int past = window == 0 ? 0 : int(max(0ll, (long long)pos - window + 1));
+          const uint32_t hole4[4] = {hole.x, hole.y, hole.z, hole.w};
 #pragma unroll
           for (int i = 0; i < G::kKeys / 32; ++i) {
             const int from = key0 + 32 * i;
             const uint32_t seen =
-                below(pos + 1 - from) & (~below(past - from) | below(sinks - from)) & ~hole[i];
+                below(pos + 1 - from) & (~below(past - from) | below(sinks - from)) & ~hole4[i];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (!((seen >> j) & 1)) raw[32 * i + j] = __float_as_uint(kNegInf);
           }
         }
-        float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        // NaN if any score is
+        float top[2] = {kNegInf, kNegInf};
 #pragma unroll
-        for (int j = 0; j < G::kKeys; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(raw[j]));
-        const float most =
-            fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
-        const bool move = most > m + kSlack || (m == kNegInf && most > kNegInf);
+        for (int j = 0; j < G::kKeys; j += 4) {
+          top[0] = max3_nan(top[0], __uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
+          top[1] = max3_nan(top[1], __uint_as_float(raw[j + 2]), __uint_as_float(raw[j + 3]));
+        }
+        const float most = max3_nan(top[0], top[1], kNegInf) * p.scale_log2;
+        const bool move = !(most <= m + kSlack);
         if (__any_sync(~0u, move)) {
-          const float next = move ? most : m;
+          const float next = move ? max3_nan(m, most, kNegInf) : m;
           const float f = m == next ? 1.f : exp2_fast(m - next);
           m = next;
           l *= f;
-          if (u > w.first) {
+          if (u > first) {
             // the products into O so far are done: S came after them
             for (int c = 0; c < D; c += 16) {
               uint32_t o[16];
@@ -270,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float shift = m == kNegInf ? 0.f : -m;
+        // NaN for a maximum that is not finite: the polynomial would not show it
+        const float shift = m == kNegInf ? 0.f : (m - m) - m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         const float2 shift2 = make_float2(shift, shift);
@@ -299,17 +324,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the rows' output
-      const bool none = w.first >= w.last;
+      const bool none = first >= last;
       if (!none) {
         if (!(ok = mbar_wait(bar.o_full + 8 * tile, o_phase, dead))) break;
         o_phase ^= 1;
         tc_fence_after();
       }
+      const int tok = div_of(row, p.group_div);
+      const int64_t t = it.token0 + tok;
+      const int qh = it.head * p.group + row - tok * p.group;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t piece = int64_t(w.piece) * G::kRows + 128 * tile + r;
+      const int64_t piece = int64_t(it.piece) * G::kRows + 128 * tile + r;
       const int64_t whole = (int64_t(prefix) * p.num_tokens + t) * p.q_heads + qh;
-      float* part = !w.whole ? p.tiles.pieces + piece * D : p.whole + whole * D;
-      const bool direct = w.whole && !p.shared;
+      float* part = !it.whole ? p.tiles.pieces + piece * D : p.whole + whole * D;
+      const bool direct = it.whole && !p.shared;
       uint16_t* out = p.out + t * p.out_stride + int64_t(qh) * D;
       bool odd = !(l - l == 0.f);
       for (int c = 0; c < D; c += 16) {
@@ -344,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (real) {
-        if (!direct) (w.whole ? p.whole_stats[whole] : p.tiles.stats[piece]) = make_float2(m, l);
+        if (!direct) (it.whole ? p.whole_stats[whole] : p.tiles.stats[piece]) = make_float2(m, l);
         else if (p.lse != nullptr) p.lse[t * p.q_heads + qh] = log_sum(m, l);
       }
       // rows whose sums are not finite, where some keys were hidden
@@ -355,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         again &= again - 1;
         const int rr = 128 * tile + 32 * (warp & 3) + src;
         float o[2][4], mm, ll;
-        recompute_row<T>(p, it, w.head, it.row + rr, G::kKeys, w.first, w.last, o, mm, ll);
+        recompute_row<T>(p, it, it.row + rr, G::kKeys, o, mm, ll);
         const float scale = direct ? (ll == 0.f ? 0.f : 1.f / ll) : 1.f;
         const int64_t t2 = __shfl_sync(~0u, t, src);
         const int qh2 = __shfl_sync(~0u, qh, src);
@@ -367,15 +395,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint2*>(p.out + t2 * p.out_stride + int64_t(qh2) * D + d) = make_uint2(
                 T::pack(o[h][0] * scale, o[h][1] * scale), T::pack(o[h][2] * scale, o[h][3] * scale));
           else
-            *reinterpret_cast<float4*>((w.whole ? p.whole + whole2 * D : p.tiles.pieces + piece2 * D) +
+            *reinterpret_cast<float4*>((it.whole ? p.whole + whole2 * D : p.tiles.pieces + piece2 * D) +
                                        d) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
         }
         if (lane == 0) {
-          if (!direct) (w.whole ? p.whole_stats[whole2] : p.tiles.stats[piece2]) = make_float2(mm, ll);
+          if (!direct) (it.whole ? p.whole_stats[whole2] : p.tiles.stats[piece2]) = make_float2(mm, ll);
           else if (p.lse != nullptr) p.lse[t2 * p.q_heads + qh2] = log_sum(mm, ll);
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.item_free + 8 * (n % kItems));
     }
     if (!ok && any && tile < G::kTiles && lane == 0) report(p.status, CG_ERR_CUDA);
   } else {
@@ -388,10 +418,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t q_phase = 3;  // a bit for each query tile
       bool ok = any, noted = false;
       if (!any && lane == 0) w.note_cut(p.tiles, false);
-      while (ok && w.next(p)) {
+      for (uint32_t n = 0; ok; ++n) {
+        const bool more = w.next(p);
         const Item& it = w.it;
-        if (!noted && lane == 0) w.note_cut(p.tiles, true);
+        if (!noted && lane == 0) w.note_cut(p.tiles, more);
         noted = true;
+        if (!(ok = mbar_wait(bar.item_free + 8 * (n % kItems), ((n / kItems) & 1) ^ 1, dead))) break;
+        if (lane == 0) {
+          deals[n % kItems] = Deal{w.first, max(w.first, w.last), it.span.sink_units,
+                                   it.span.first_unit, more ? it.rows : 0, it.row, it.req.first,
+                                   it.req.row0, it.request, w.head, w.piece, w.whole};
+          mbar_arrive(bar.item_full + 8 * (n % kItems));
+        }
+        __syncwarp();
+        if (!more) break;
         if (w.first >= w.last) continue;
         for (int tile = 0; tile < (it.rows > 128 ? 2 : 1); ++tile) {
           if (!(ok = mbar_wait(bar.q_free + 8 * tile, (q_phase >> tile) & 1, dead))) break;
@@ -467,9 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < G::kKeys / 16; ++k)
           mma_ts(dst, a + 8 * k, b + (k * 2048 >> 4), pv, k > 0 || add);
       };
-      while (ok && w.next(p)) {
-        const int active = w.it.rows > 128 ? 2 : 1;
-        if (w.first >= w.last) continue;
+      for (uint32_t n = 0; ok; ++n) {
+        const Deal& it = deals[n % kItems];
+        if (!(ok = mbar_wait(bar.item_full + 8 * (n % kItems), (n / kItems) & 1, dead))) break;
+        const int rows = it.rows, first = it.first, last = it.last;
+        mbar_arrive(bar.item_free + 8 * (n % kItems));
+        if (rows == 0) break;
+        const int active = rows > 128 ? 2 : 1;
+        if (first >= last) continue;
         if (!(ok = mbar_wait(ring.full + 8 * stage, phase, dead))) break;
         uint32_t k_stage = stage;
         step();
@@ -477,12 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = mbar_wait(bar.q_full + 8 * tile, (q_phase >> tile) & 1, dead))) break;
           q_phase ^= 1u << tile;
           tc_fence_after();
-          scores(tile, k_stage, w.first + 1 == w.last);
+          scores(tile, k_stage, first + 1 == last);
         }
         if (!ok) break;
         mma_commit(ring.empty + 8 * k_stage);
-        for (int u = w.first; ok && u < w.last; ++u) {
-          const bool more = u + 1 < w.last;
+        for (int u = first; ok && u < last; ++u) {
+          const bool more = u + 1 < last;
           if (!(ok = mbar_wait(ring.full + 8 * stage, phase, dead))) break;
           const uint32_t v_stage = stage;
           step();
@@ -495,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = mbar_wait(bar.p_full + 8 * tile, (p_phase >> tile) & 1, dead))) break;
             p_phase ^= 1u << tile;
             tc_fence_after();
-            outputs(tile, v_stage, u > w.first);
-            if (more) scores(tile, k_stage, u + 2 == w.last);
+            outputs(tile, v_stage, u > first);
+            if (more) scores(tile, k_stage, u + 2 == last);
             else mma_commit(bar.o_full + 8 * tile);
           }
           if (!ok) break;

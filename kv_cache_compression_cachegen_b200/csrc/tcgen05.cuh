@@ -175,6 +175,13 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&d);
 }
 
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // ---- matrix products
 
 // Shared-memory operand in the 128-byte swizzle (16-byte chunk index xor row
