@@ -8,7 +8,7 @@
 //   warps 10, 11     K and V from the pages to shared memory (kv_loader.cuh)
 //   warp 9           deals the items; queries to shared memory, as soon as the
 //                    last product with the item's before has read them
-//   warp 8           one thread issues the products:
+//   warp 8           issues the products:
 //                      S = Q K^T   both operands in shared memory
 //                      O += P V    P in tensor memory, V along its channels
 // The two query tiles take turns: while one's scores are in softmax the tensor
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_mem;
   __shared__ __align__(16) uint32_t no_page[4][4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t q_smem = base;
   const uint32_t kv_smem = base + G::kTiles * DC * G::kQBytes;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(~0u, tmem_slot, 0);
   const int D = p.dim;
 
   if (warp < 8) {
@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = mbar_wait(bar.item_full + 8 * (n % kItems), (n / kItems) & 1, dead))) break;
       if (it.rows == 0) break;
       const int first = it.first, last = it.last;
+      const int sink_units = it.sink_units, key_shift = (it.first_unit - it.sink_units) * G::kKeys;
       if (it.rows <= 128 * tile) {  // no rows in this tile
         unit_count += last - first;
         __syncwarp();
@@ -248,8 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t raw[G::kKeys];
 #pragma unroll
         for (int j = 0; j < G::kKeys; j += 64) tmem_load64(t_s + j, raw + j);
-        const int key0 =
-            (u < it.sink_units ? u : it.first_unit + u - it.sink_units) * G::kKeys;
+        const int key0 = u * G::kKeys + (u < sink_units ? 0 : key_shift);
         // the whole unit is seen by the row, or its keys are hidden one by one
         const int end = key0 + G::kKeys - 1;
         const uint4 hole = *reinterpret_cast<const uint4*>(no_page[unit_count & 3]);
@@ -471,13 +471,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar.q_full + 8 * tile);
         }
       }
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
       // ---- the products
       constexpr bool kBf16 = T::kBf16;
       const uint32_t qk = mma_desc(kBf16, false, 128, G::kKeys);
       const uint32_t pv = mma_desc(kBf16, true, 128, DC == 2 ? 128 : D);
       uint32_t stage = 0, phase = 0, q_phase = 0, p_phase = 0;  // a bit for each query tile
-      bool ok = any;
+      bool ok = __shfl_sync(~0u, any, 0);
+      const auto wait = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(~0u, mbar_wait(b, parity, dead)) != 0;
+      };
       const auto step = [&]() {
         if (++stage == G::kStages) stage = 0, phase ^= 1;
       };
@@ -509,17 +512,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (uint32_t n = 0; ok; ++n) {
         const Deal& it = deals[n % kItems];
-        if (!(ok = mbar_wait(bar.item_full + 8 * (n % kItems), (n / kItems) & 1, dead))) break;
-        const int rows = it.rows, first = it.first, last = it.last;
-        mbar_arrive(bar.item_free + 8 * (n % kItems));
+        if (!(ok = wait(bar.item_full + 8 * (n % kItems), (n / kItems) & 1))) break;
+        // from lane 0: the same in all lanes, as the compiler can see
+        const int rows = __shfl_sync(~0u, it.rows, 0);
+        const int first = __shfl_sync(~0u, it.first, 0), last = __shfl_sync(~0u, it.last, 0);
+        if (lane == 0) mbar_arrive(bar.item_free + 8 * (n % kItems));
         if (rows == 0) break;
         const int active = rows > 128 ? 2 : 1;
         if (first >= last) continue;
-        if (!(ok = mbar_wait(ring.full + 8 * stage, phase, dead))) break;
+        if (!(ok = wait(ring.full + 8 * stage, phase))) break;
         uint32_t k_stage = stage;
         step();
         for (int tile = 0; tile < active; ++tile) {
-          if (!(ok = mbar_wait(bar.q_full + 8 * tile, (q_phase >> tile) & 1, dead))) break;
+          if (!(ok = wait(bar.q_full + 8 * tile, (q_phase >> tile) & 1))) break;
           q_phase ^= 1u << tile;
           tc_fence_after();
           scores(tile, k_stage, first + 1 == last);
@@ -528,16 +533,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(ring.empty + 8 * k_stage);
         for (int u = first; ok && u < last; ++u) {
           const bool more = u + 1 < last;
-          if (!(ok = mbar_wait(ring.full + 8 * stage, phase, dead))) break;
+          if (!(ok = wait(ring.full + 8 * stage, phase))) break;
           const uint32_t v_stage = stage;
           step();
           if (more) {
-            if (!(ok = mbar_wait(ring.full + 8 * stage, phase, dead))) break;
+            if (!(ok = wait(ring.full + 8 * stage, phase))) break;
             k_stage = stage;
             step();
           }
           for (int tile = 0; tile < active; ++tile) {
-            if (!(ok = mbar_wait(bar.p_full + 8 * tile, (p_phase >> tile) & 1, dead))) break;
+            if (!(ok = wait(bar.p_full + 8 * tile, (p_phase >> tile) & 1))) break;
             p_phase ^= 1u << tile;
             tc_fence_after();
             outputs(tile, v_stage, u > first);
