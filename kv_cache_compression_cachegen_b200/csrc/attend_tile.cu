@@ -303,9 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < G::kKeys; j += 2) {
           const float2 x = fma_pair(
               make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])), scale2, shift2);
-          // three of eight on the multiply-add pipe: see exp2_pair
-          const int turn = (j >> 1) & 7;
-          const float2 e = turn == 1 || turn == 4 || turn == 6
+          // a quarter on the multiply-add pipe: see exp2_pair
+          const float2 e = (j & 7) == 4
                                ? exp2_pair(x)
                                : make_float2(exp2_fast(x.x), exp2_fast(x.y));
           sum[(j >> 1) & 1] = add_pair(sum[(j >> 1) & 1], e);
@@ -440,12 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row0 = it.row + 128 * tile;
           if (by_map) {
             // rows behind the item's are other tokens' or zeros, and are not used
-            if (lane == 0) {
-              mbar_expect(bar.q_full + 8 * tile, DC * G::kQBytes);
-              for (int b = 0; b < DC; ++b)
-                tma_load3(dst + b * G::kQBytes, &q_map, 64 * b, w.head * p.group,
-                          it.req.first + div_of(row0, p.group_div), bar.q_full + 8 * tile);
-            }
+            mbar_expect(bar.q_full + 8 * tile, DC * G::kQBytes);
+            const int head = __shfl_sync(~0u, w.head * p.group, 0);
+            const int token = __shfl_sync(~0u, it.req.first + div_of(row0, p.group_div), 0);
+            for (int b = 0; b < DC; ++b)
+              tma_load3(dst + b * G::kQBytes, &q_map, 64 * b, head, token, bar.q_full + 8 * tile);
             continue;
           }
 #pragma unroll 4
@@ -546,11 +544,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             p_phase ^= 1u << tile;
             tc_fence_after();
             outputs(tile, v_stage, u > first);
+            if (tile + 1 == active) mma_commit(ring.empty + 8 * v_stage);
             if (more) scores(tile, k_stage, u + 2 == last);
             else mma_commit(bar.o_full + 8 * tile);
           }
           if (!ok) break;
-          mma_commit(ring.empty + 8 * v_stage);
           if (more) mma_commit(ring.empty + 8 * k_stage);
         }
       }

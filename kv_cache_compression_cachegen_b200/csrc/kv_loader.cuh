@@ -45,12 +45,13 @@ __device__ __forceinline__ bool load_kv(const AttnParams& p, Walk<kTile, kKeys>&
   const int lane = threadIdx.x & 31;
   const int c = lane % kLanes, sub = lane / kLanes, D = p.dim;
   const int64_t step = int64_t(p.kv_heads) * D;
-  const int boxes = box > 0 ? kMine / box * DC : 0;
-  uint32_t stage = 0, phase = 1, tiles = 0, unit_count = 0;
+  uint32_t stage = 0, phase = 1, unit_count = 0;
   uint32_t copied = 0;  // the latest tiles, a bit each: this warp's half came by cp.async
   bool ok = true;
-  const auto pass_on = [&](uint32_t behind) {
+  const auto pass_on = [&](int behind) {
     if ((copied >> (behind - 1)) & 1) {
+      if (behind == kLag) cp_async_wait<kLag>();
+      else cp_async_wait<0>();
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(ring.full + 8 * ((stage + kStages - behind) % kStages));
@@ -60,20 +61,21 @@ __device__ __forceinline__ bool load_kv(const AttnParams& p, Walk<kTile, kKeys>&
     const Item& it = w.it;
     const bool prefix = it.request < 0;
     const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
-    const int64_t col = int64_t(w.head) * D + 8 * c;
+    const int head = __shfl_sync(~0u, w.head, 0);
+    const int64_t col = int64_t(head) * D + 8 * c;
     // Lane i has the warp's keys i, i + 32, ... of the unit; their pages are
-    // looked up a unit ahead.  -2: no row of the item sees the key.
+    // looked up a unit ahead.  Key -1: no row of the item sees it.
     int key_ahead[kOwn], page_ahead[kOwn], mine[kOwn];
     const auto look_up = [&](int u) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        page_ahead[i] = -2;
-        key_ahead[i] = 0;
+        key_ahead[i] = -1;
         if (u < w.last) {
           const int key = unit_key<kKeys>(it.span, u) + kMine * wk + 32 * i + lane;
-          if (key < it.span.hi && (key >= it.span.lo || key < it.span.sink_end))
-            page_ahead[i] = max(-1, __ldg(table + div_of(key, p.page_div)));
-          key_ahead[i] = key;
+          if (key < it.span.hi && (key >= it.span.lo || key < it.span.sink_end)) {
+            key_ahead[i] = key;
+            page_ahead[i] = __ldg(table + div_of(key, p.page_div));
+          }
         }
       }
     };
@@ -83,9 +85,10 @@ __device__ __forceinline__ bool load_kv(const AttnParams& p, Walk<kTile, kKeys>&
       bool there = box > 0;  // every key of the warp's half can be read
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        const bool hole = page_ahead[i] == -1 || page_ahead[i] >= p.num_pages;
+        const bool sees_it = key_ahead[i] >= 0;
+        const bool hole = sees_it && (page_ahead[i] < 0 || page_ahead[i] >= p.num_pages);
         mine[i] = -1;
-        if (page_ahead[i] >= 0 && !hole)
+        if (sees_it && !hole)
           mine[i] = page_ahead[i] * p.page_tokens +
                     (key_ahead[i] - div_of(key_ahead[i], p.page_div) * p.page_tokens);
         holes[i] = __ballot_sync(~0u, hole);
@@ -93,30 +96,32 @@ __device__ __forceinline__ bool load_kv(const AttnParams& p, Walk<kTile, kKeys>&
         if (holes[i] != 0 && lane == 0) report(p.status, CG_ERR_MISMATCH);
       }
       there = __all_sync(~0u, there);
+      int rows[kMine / 8];  // of the boxes: before the copies, which keep their order
+#pragma unroll
+      for (int i = 0; i < kMine / 8; ++i) {
+        const int key = i * box;
+        rows[i] = __shfl_sync(~0u, kOwn == 2 && key >= 32 ? mine[kOwn - 1] : mine[0], key & 31);
+      }
       look_up(u + 1);
       for (int kv = 0; kv < 2; ++kv) {
-        if (!(ok = mbar_wait(ring.empty + 8 * stage, phase, ring.dead))) break;
-        if (kv == 0 && lane == 0) {
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i) ring.no_page[unit_count & 3][wk * kOwn + i] = holes[i];
-        }
-        __syncwarp();
+        // the same in all lanes, as the compiler can see: addresses stay uniform
+        ok = __all_sync(~0u, mbar_wait(ring.empty + 8 * stage, phase, ring.dead));
+        if (!ok) break;
+        if (kv == 0 && lane < kOwn)
+          ring.no_page[unit_count & 3][wk * kOwn + lane] = lane == 0 ? holes[0] : holes[kOwn - 1];
         const uint32_t tile = ring.smem + stage * kStage;
         if (there) {
           // whole boxes of keys that follow one another in a page
-          if (lane == 0) mbar_expect(ring.full + 8 * stage, kMine * 128 * DC);
           __syncwarp();
-          for (int i0 = 0; i0 < boxes; i0 += 32) {
-            const int i = i0 + lane, b = i % DC, key = i / DC * box;
-            int row = __shfl_sync(~0u, mine[0], key & 31);
-            if constexpr (kOwn == 2) {
-              const int upper = __shfl_sync(~0u, mine[kOwn - 1], key & 31);
-              if (key >= 32) row = upper;
+          mbar_expect(ring.full + 8 * stage, kMine * 128 * DC);
+#pragma unroll
+          for (int i = 0; i < kMine / 8; ++i)
+            if (i * box < kMine) {
+#pragma unroll
+              for (int b = 0; b < DC; ++b)
+                tma_load3(tile + b * kBlock + (kMine * wk + i * box) * 128, kv ? v_map : k_map,
+                          64 * b, head, rows[i], ring.full + 8 * stage);
             }
-            if (i < boxes)
-              tma_load3(tile + b * kBlock + (kMine * wk + key) * 128, kv ? v_map : k_map, 64 * b,
-                        w.head, row, ring.full + 8 * stage);
-          }
         } else {
           const uint16_t* pool = (kv ? p.v_pool : p.k_pool) + col;
           const uint32_t dst = tile + (c >> 3) * kBlock;
@@ -138,22 +143,16 @@ __device__ __forceinline__ bool load_kv(const AttnParams& p, Walk<kTile, kKeys>&
             }
         }
         cp_async_commit();
-        if (tiles >= kLag) {
-          cp_async_wait<kLag>();
-          pass_on(kLag);
-        }
+        pass_on(kLag);
         copied = (copied << 1) | (there ? 0u : 1u);
-        ++tiles;
         if (++stage == kStages) stage = 0, phase ^= 1;
       }
     }
   }
-  if (kLag > 1 && tiles > 1) {
-    cp_async_wait<1>();
-    pass_on(2);
-  }
+  // the last ones: nothing follows them
   cp_async_wait<0>();
-  if (tiles > 0) pass_on(1);
+  if (kLag > 1) pass_on(2);
+  pass_on(1);
   return ok;
 }
 
@@ -164,14 +163,14 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
                                            const CUtensorMap* v_map, int box, int wk) {
   constexpr int kBlock = kKeys * 128, kStage = DC * kBlock;
   constexpr int kMine = kKeys / kLoadWarps;
-  static_assert(kMine / 8 * DC <= 32 && kMine <= 64, "a lane has at most one box");
+  static_assert(kMine / 8 <= 32 && kMine <= 64, "a lane has at most one box's keys");
   const int lane = threadIdx.x & 31;
-  const int b = lane % DC, own = lane / DC * box;  // the lane's box: channels, first key
+  const int own = lane * box;  // the lane's keys: its box's first
   uint32_t stage = 0, phase = 1, unit_count = 0;
-  // One unit: where the lane's box lies; looked up while the unit before is issued.
+  // One unit: where the lane's keys lie; looked up while the unit before is issued.
   struct Ahead {
-    int page, row_in_page, head;  // page -2: no row of the item sees the box
-    bool unit;
+    int page, row_in_page, head;
+    bool unit, seen;  // seen: some row of the item sees some of the keys
   } next;
   const int32_t* table = nullptr;
   int u = 0;
@@ -187,24 +186,28 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
       table = w.it.request < 0 ? p.prefix_table : p.tables + int64_t(w.it.request) * p.max_pages;
     }
     const int key = unit_key<kKeys>(w.it.span, u) + kMine * wk + own;
-    next.page = -2;
     next.head = w.head;
-    if (own < kMine && key < w.it.span.hi &&
-        (key + box > w.it.span.lo || key < w.it.span.sink_end)) {
+    next.seen = own < kMine && key < w.it.span.hi &&
+                (key + box > w.it.span.lo || key < w.it.span.sink_end);
+    if (next.seen) {
       const int col = div_of(key, p.page_div);
       next.row_in_page = key - col * p.page_tokens;
-      next.page = max(-1, __ldg(table + col));
+      next.page = __ldg(table + col);
     }
     ++u;
   };
   look_up();
-  for (; next.unit; ++unit_count) {
+  while (__all_sync(~0u, next.unit)) {
     const Ahead now = next;
     look_up();
-    const bool hole = now.page == -1 || now.page >= p.num_pages;
-    const bool mine = now.page >= 0 && !hole;
-    const int row = mine ? now.page * p.page_tokens + now.row_in_page : 0;
-    const uint32_t bytes = __popc(__ballot_sync(~0u, mine)) * box * 128;
+    const bool hole = now.seen && (now.page < 0 || now.page >= p.num_pages);
+    const bool mine = now.seen && !hole;
+    const int row = now.page * p.page_tokens + now.row_in_page;
+    const uint32_t there = __ballot_sync(~0u, mine);
+    const int head = __shfl_sync(~0u, now.head, 0);
+    int rows[kMine / 8];  // before the copies, which keep their order
+#pragma unroll
+    for (int i = 0; i < kMine / 8; ++i) rows[i] = __shfl_sync(~0u, row, i);
     uint32_t holes[2] = {0, 0};
     if (__any_sync(~0u, hole)) {
       const uint64_t bits = hole ? (box < 64 ? (1ull << box) - 1 : ~0ull) << own : 0ull;
@@ -213,21 +216,23 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
       if (lane == 0) report(p.status, CG_ERR_MISMATCH);
     }
     for (int kv = 0; kv < 2; ++kv) {
-      if (!mbar_wait(ring.empty + 8 * stage, phase, ring.dead)) return false;
-      if (lane == 0) {
-        if (kv == 0) {
-#pragma unroll
-          for (int i = 0; i < kMine / 32; ++i)
-            ring.no_page[unit_count & 3][wk * (kMine / 32) + i] = holes[i];
-        }
-        mbar_expect(ring.full + 8 * stage, bytes);
-      }
+      if (!__all_sync(~0u, mbar_wait(ring.empty + 8 * stage, phase, ring.dead))) return false;
+      if (kv == 0 && lane < kMine / 32)
+        ring.no_page[unit_count & 3][wk * (kMine / 32) + lane] = holes[lane & 1];
       __syncwarp();
-      if (mine)
-        tma_load3(ring.smem + stage * kStage + b * kBlock + (kMine * wk + own) * 128,
-                  kv ? v_map : k_map, 64 * b, now.head, row, ring.full + 8 * stage);
+      mbar_expect(ring.full + 8 * stage, __popc(there) * box * (128 * DC));
+      const uint32_t dst = ring.smem + stage * kStage + kMine * wk * 128;
+#pragma unroll
+      for (int i = 0; i < kMine / 8; ++i)
+        if ((there >> i) & 1) {
+#pragma unroll
+          for (int b = 0; b < DC; ++b)
+            tma_load3(dst + b * kBlock + i * box * 128, kv ? v_map : k_map, 64 * b, head, rows[i],
+                      ring.full + 8 * stage);
+        }
       if (++stage == kStages) stage = 0, phase ^= 1;
     }
+    ++unit_count;
   }
   return true;
 }

@@ -72,16 +72,23 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // ---- tensor copies
 
-// Arrive, and have the phase wait for `bytes` more of tensor copies.
+// Arrive once, and have the phase wait for `bytes` more of tensor copies; by a
+// whole warp.
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
+  asm volatile(
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
 }
+// By a whole warp with the same arguments, issued by one lane: lanes with
+// arguments of their own would be taken one after another, 80 cycles each.
 __device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, int y, int z,
                                           uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4}], [%5];" ::"r"(dst),
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "@e cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
