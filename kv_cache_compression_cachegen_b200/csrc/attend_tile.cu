@@ -51,7 +51,8 @@ struct Geometry {
 };
 
 struct Bars {
-  uint32_t q_full, q_free, s_full, p_full, o_full;  // each the first of its two
+  uint32_t q_full, q_free, s_full, o_full;  // each the first of its two
+  uint32_t p_full;                          // of the halves of each tile's weights
   uint32_t item_full, item_free;                    // of kItems
 };
 
@@ -66,12 +67,14 @@ struct Deal {
   int head, piece, whole;
 };
 
-// 2^x of two values without the special-function unit, which alone would take
-// as long over a unit's weights as the tensor cores over its products: n =
-// round(x) by adding 1.5 * 2^23, a polynomial for 2^(x - n) on [-1/2, 1/2], n
-// added to the exponent.  The coefficients are the minimax ones of degree 5 for
-// the relative error (Remez exchange), 2^-23.7, and 2^-22 as evaluated in fp32
-// -- what ex2.approx has.  Below -125 the result stays 2^-125.
+// 2^x of two values without the special-function unit, for the eighth of a
+// unit's weights that the multiply-add pipe has time for: n = round(x) by adding
+// 1.5 * 2^23, a polynomial for 2^(x - n) on [-1/2, 1/2], n added to the exponent.
+// The coefficients are the minimax ones of degree 5 for the relative error (Remez
+// exchange), 2^-23.7, and 2^-22 as evaluated in fp32 -- what ex2.approx has.
+// Below -125 the result stays 2^-125.  (Of a unit's 128 weights a row, none to
+// three eighths were tried: an eighth is as fast as a quarter or faster
+// everywhere, and a tenth faster than none on short items.)
 __device__ __forceinline__ float2 exp2_pair(float2 x) {
   const float2 magic = make_float2(12582912.f, 12582912.f);
   const float2 minus = make_float2(-12582912.f, -12582912.f);
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap q_map, int by_map) {
   using G = Geometry<DC>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars_mem[2 * G::kStages + 10 + 2 * kItems];
+  __shared__ uint64_t bars_mem[2 * G::kStages + 12 + 2 * kItems];
   __shared__ Deal deals[kItems];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_mem;
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bar.q_free = bar.q_full + 16;
   bar.s_full = bar.q_free + 16;
   bar.p_full = bar.s_full + 16;
-  bar.o_full = bar.p_full + 16;
+  bar.o_full = bar.p_full + 32;
   bar.item_full = bar.o_full + 16;
   bar.item_free = bar.item_full + 8 * kItems;
 
@@ -196,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar.q_full + 8 * i, 1);
       mbar_init(bar.q_free + 8 * i, 1);
       mbar_init(bar.s_full + 8 * i, 1);
-      mbar_init(bar.p_full + 8 * i, 4);
+      mbar_init(bar.p_full + 16 * i, 4);
+      mbar_init(bar.p_full + 16 * i + 8, 4);
       mbar_init(bar.o_full + 8 * i, 1);
     }
     for (int i = 0; i < kItems; ++i) {
@@ -243,18 +247,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = kNegInf, l = 0.f;
       bool mixed = false;  // some unit had keys that a row does not see
       for (int u = first; u < last; ++u, ++unit_count) {
-        if (!(ok = mbar_wait(bar.s_full + 8 * tile, s_phase, dead))) break;
-        s_phase ^= 1;
-        tc_fence_after();
-        uint32_t raw[G::kKeys];
-#pragma unroll
-        for (int j = 0; j < G::kKeys; j += 64) tmem_load64(t_s + j, raw + j);
         const int key0 = u * G::kKeys + (u < sink_units ? 0 : key_shift);
         // the whole unit is seen by the row, or its keys are hidden one by one
         const int end = key0 + G::kKeys - 1;
+        const bool full = __all_sync(
+            ~0u, end <= pos && (window == 0 || pos - key0 < window || end < sinks));
+        if (!(ok = mbar_wait(bar.s_full + 8 * tile, s_phase, dead))) break;
+        s_phase ^= 1;
+        tc_fence_after();
         const uint4 hole = *reinterpret_cast<const uint4*>(no_page[unit_count & 3]);
-        const bool full = end <= pos && (window == 0 || pos - key0 < window || end < sinks);
-        if (!__all_sync(~0u, full && (hole.x | hole.y | hole.z | hole.w) == 0)) {
+        uint32_t raw[G::kKeys];
+        tmem_load<G::kKeys>(t_s, raw);
+        if (!full || (hole.x | hole.y | hole.z | hole.w) != 0) {
           mixed = true;
           // keys before `past` are behind the window
           const int past = window == 0 ? 0 : int(max(0ll, (long long)pos - window + 1));
@@ -299,27 +303,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         const float2 shift2 = make_float2(shift, shift);
+        // By halves of the unit, so that the product with the first half's values
+        // runs while the second half is computed.
 #pragma unroll
-        for (int j = 0; j < G::kKeys; j += 2) {
-          const float2 x = fma_pair(
-              make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])), scale2, shift2);
-          // a quarter on the multiply-add pipe: see exp2_pair
-          const float2 e = (j & 7) == 4
-                               ? exp2_pair(x)
-                               : make_float2(exp2_fast(x.x), exp2_fast(x.y));
-          sum[(j >> 1) & 1] = add_pair(sum[(j >> 1) & 1], e);
-          // rounded to the pool's type for the product with V: half a step of it
-          // relative to each weight; the sum is not
-          raw[j / 2] = T::pack(e.x, e.y);
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = h * (G::kKeys / 2); j < (h + 1) * (G::kKeys / 2); j += 2) {
+            const float2 x = fma_pair(
+                make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])), scale2, shift2);
+            // a sixteenth on the multiply-add pipe: see exp2_pair
+            const float2 e = (j & 31) == 8 ? exp2_pair(x)
+                                           : make_float2(exp2_fast(x.x), exp2_fast(x.y));
+            sum[(j >> 1) & 1] = add_pair(sum[(j >> 1) & 1], e);
+            // rounded to the pool's type for the product with V: half a step of it
+            // relative to each weight; the sum is not
+            raw[j / 2] = T::pack(e.x, e.y);
+          }
+          constexpr int kColumns = G::kKeys / 4;
+          if constexpr (kColumns == 32) tmem_store32(t_p + h * kColumns, raw + h * kColumns);
+          else tmem_store16(t_p + h * kColumns, raw + h * kColumns);
+          tmem_store_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.p_full + 8 * (2 * tile + h));
         }
         // nothing seen so far: exp2_pair leaves 2^-125 where the weight is zero
         l = m == kNegInf ? 0.f : l + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
-#pragma unroll
-        for (int j = 0; j < G::kKeys / 2; j += 32) tmem_store32(t_p + j, raw + j);
-        tmem_store_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.p_full + 8 * tile);
       }
       if (!ok) break;
       // ---- the rows' output
@@ -500,12 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(bar.s_full + 8 * tile);
         if (final) mma_commit(bar.q_free + 8 * tile);
       };
-      const auto outputs = [&](int tile, uint32_t at, bool add) {
+      const auto outputs = [&](int tile, uint32_t at, int half, bool add) {
         const uint32_t dst = tmem + G::kO + tile * G::kOStep;
-        const uint32_t a = tmem + G::kP + tile * G::kPStep;
-        const uint64_t b = v_desc + at * (G::kStage >> 4);
+        const uint32_t a = tmem + G::kP + tile * G::kPStep + half * (G::kKeys / 4);
+        const uint64_t b = v_desc + at * (G::kStage >> 4) + half * (G::kKeys / 2 * 128 >> 4);
 #pragma unroll
-        for (int k = 0; k < G::kKeys / 16; ++k)
+        for (int k = 0; k < G::kKeys / 32; ++k)
           mma_ts(dst, a + 8 * k, b + (k * 2048 >> 4), pv, k > 0 || add);
       };
       for (uint32_t n = 0; ok; ++n) {
@@ -540,10 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             step();
           }
           for (int tile = 0; tile < active; ++tile) {
-            if (!(ok = wait(bar.p_full + 8 * tile, (p_phase >> tile) & 1))) break;
+            if (!(ok = wait(bar.p_full + 16 * tile, (p_phase >> tile) & 1))) break;
+            tc_fence_after();
+            outputs(tile, v_stage, 0, u > first);
+            if (!(ok = wait(bar.p_full + 16 * tile + 8, (p_phase >> tile) & 1))) break;
             p_phase ^= 1u << tile;
             tc_fence_after();
-            outputs(tile, v_stage, u > first);
+            outputs(tile, v_stage, 1, true);
             if (tile + 1 == active) mma_commit(ring.empty + 8 * v_stage);
             if (more) scores(tile, k_stage, u + 2 == last);
             else mma_commit(bar.o_full + 8 * tile);

@@ -105,7 +105,7 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 
-// The loads wait in the same statement, so no use can be scheduled before the data is there.
+// The load waits in the same statement, so no use can come before the data.
 __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
@@ -118,7 +118,9 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load64(uint32_t addr, uint32_t* r) {
+// Columns of the warp's 32 lanes to registers.  A use of the registers must not
+// be moved before the wait: the empty statements behind it tie them to it.
+__device__ __forceinline__ void tmem_ask64(uint32_t addr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -126,7 +128,6 @@ __device__ __forceinline__ void tmem_load64(uint32_t addr, uint32_t* r) {
       "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
       "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
       "}, [%64];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
       :
         "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
@@ -138,6 +139,20 @@ __device__ __forceinline__ void tmem_load64(uint32_t addr, uint32_t* r) {
         "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tie16(uint32_t* r) {
+  asm volatile(""
+      :
+        "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 64) tmem_ask64(addr + i, r + i);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 16) tie16(r + i);
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
   asm volatile(
