@@ -9,6 +9,7 @@ namespace cg {
 namespace {
 
 constexpr int kMaxCtas = 160;  // of either kernel, one an SM
+constexpr int64_t kInStepBytes = 64 << 20;  // half of the L2 cache
 
 // Block 0 sums up the rows kernel's line, block 1 the tile kernel's.
 template <int kTile, int kKeys>
@@ -136,7 +137,7 @@ __device__ __forceinline__ Part find_part(const AttnParams& p, const Lane& line,
   part.in_tile = row % kTile;
   const int64_t cum = line.cum[x], cost = line.cum[x + 1] - cum;
   const int64_t units = line.cum[total_slots<kTile>(p)] * p.kv_heads;
-  const int ctas = shares_of(line, units);
+  const int ctas = shares_of<kTile>(p, line, units);
   const int64_t item0 = cum * p.kv_heads + head * cost;
   part.c0 = cta_of(item0, units, ctas);
   part.c1 = cta_of(item0 + cost - 1, units, ctas);
@@ -213,6 +214,8 @@ cudaError_t launch_all(AttnParams& p, int sms, cudaStream_t stream) {
   const bool tiles = p.tiled || (p.shared && !p.prefix_small);
   p.tiles.ctas = tiles ? std::min(kMaxCtas, sms) : 0;
   p.tiles.tile = kTile;
+  p.tiles.in_step = p.shared && !p.tiled && !p.prefix_small &&
+                    int64_t(p.prefix_tokens) * p.kv_heads * p.dim * 4 > kInStepBytes;
   const int64_t rows = int64_t(p.num_tokens) * p.group;
   const int64_t slots = (tiles ? 2 * (rows / kTile) : 0) + p.num_requests + 1;
   p.planned = slots > kScanSlots;

@@ -205,9 +205,6 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
     const int row = now.page * p.page_tokens + now.row_in_page;
     const uint32_t there = __ballot_sync(~0u, mine);
     const int head = __shfl_sync(~0u, now.head, 0);
-    int rows[kMine / 8];  // before the copies, which keep their order
-#pragma unroll
-    for (int i = 0; i < kMine / 8; ++i) rows[i] = __shfl_sync(~0u, row, i);
     uint32_t holes[2] = {0, 0};
     if (__any_sync(~0u, hole)) {
       const uint64_t bits = hole ? (box < 64 ? (1ull << box) - 1 : ~0ull) << own : 0ull;
@@ -222,14 +219,14 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
       __syncwarp();
       mbar_expect(ring.full + 8 * stage, __popc(there) * box * (128 * DC));
       const uint32_t dst = ring.smem + stage * kStage + kMine * wk * 128;
+      // A lane asks for its own box.  (One lane asking for all in turn, as above,
+      // leaves 128 single tokens behind a 4,096 window at 364 us, this at 338.)
+      if (mine) {
 #pragma unroll
-      for (int i = 0; i < kMine / 8; ++i)
-        if ((there >> i) & 1) {
-#pragma unroll
-          for (int b = 0; b < DC; ++b)
-            tma_load3(dst + b * kBlock + i * box * 128, kv ? v_map : k_map, 64 * b, head, rows[i],
-                      ring.full + 8 * stage);
-        }
+        for (int b = 0; b < DC; ++b)
+          tma_load3_own(dst + b * kBlock + lane * box * 128, kv ? v_map : k_map, 64 * b, head, row,
+                        ring.full + 8 * stage);
+      }
       if (++stage == kStages) stage = 0, phase ^= 1;
     }
     ++unit_count;

@@ -81,8 +81,16 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
       "r"(bytes)
       : "memory");
 }
-// By a whole warp with the same arguments, issued by one lane: lanes with
-// arguments of their own would be taken one after another, 80 cycles each.
+// A box of a tensor map to shared memory; by any thread.
+__device__ __forceinline__ void tma_load3_own(uint32_t dst, const void* map, int x, int y, int z,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// The same by a whole warp with the same arguments, issued by one lane.
 __device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, int y, int z,
                                           uint32_t bar) {
   asm volatile(
