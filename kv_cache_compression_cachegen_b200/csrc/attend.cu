@@ -171,6 +171,20 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(AttnParams p)
   join_row<T, kTile == 256 ? 4 : 8>(p, part, t, qh);
 }
 
+// Of the current device.
+cudaError_t multiprocessors(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms == 0) {
+    err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  }
+  return err;
+}
+
 uint64_t up256(uint64_t v) { return (v + 255) & ~uint64_t(255); }
 
 struct Workspace {
@@ -253,9 +267,8 @@ uint64_t attention_workspace(const cg_shape& s, int32_t num_q_heads, int32_t max
 cudaError_t launch_attention(const cg_attention_args& a, const cg_shape& s,
                              const int32_t* prefix_table, int32_t prefix_tokens, bool shared,
                              cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  const cudaError_t err = multiprocessors(&sms);
   if (err != cudaSuccess) return err;
   AttnParams p{};
   p.q = a.q_dev;

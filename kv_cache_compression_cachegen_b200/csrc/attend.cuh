@@ -21,6 +21,7 @@
 // every sum is fixed.
 #pragma once
 
+#include <atomic>
 #include <cuda.h>  // tensor-map types only; the encoder is looked up at run time
 
 #include "paged.cuh"
@@ -411,6 +412,19 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 // wait for the one before to have finished and written its results.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Allow a kernel its dynamic shared memory, once on each device.
+template <typename... Args>
+cudaError_t allow_smem(void (*kernel)(Args...), int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
 
 template <typename... Args>
 cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem,

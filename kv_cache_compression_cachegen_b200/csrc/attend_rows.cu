@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int DC, int NR>
 cudaError_t launch(const AttnParams& p, bool early, cudaStream_t stream) {
   using S = Shape<DC>;
-  const cudaError_t err = cudaFuncSetAttribute(
-      rows_kernel<T, DC, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t err = allow_smem(rows_kernel<T, DC, NR>, S::kSmem, done);
   if (err != cudaSuccess) return err;
   return launch_after(rows_kernel<T, DC, NR>, p.rows.ctas, kThreads, S::kSmem, stream, early, p,
                       kv_maps(p, kRowKeys / kLoadWarps, T::kBf16));

@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int DC>
 cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   using G = Geometry<DC>;
-  const cudaError_t err = cudaFuncSetAttribute(
-      tile_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t err = allow_smem(tile_kernel<T, DC>, G::kSmem, done);
   if (err != cudaSuccess) return err;
   CUtensorMap q_map{};
   const int by_map = query_map(&q_map, p, T::kBf16);

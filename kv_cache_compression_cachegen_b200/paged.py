@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -24,62 +25,74 @@ from . import (CG_DTYPE_BF16, CG_DTYPE_F16, AppendArgs, AttentionArgs, ExtendArg
                cg_attention_workspace_bytes, check, library)
 
 # torch.int16 holds fp16 bits, as everywhere in this package
-_DTYPES = {torch.float16: CG_DTYPE_F16, torch.int16: CG_DTYPE_F16,
-           torch.bfloat16: CG_DTYPE_BF16}
+_DTYPES = {torch.float16: (CG_DTYPE_F16, (torch.float16, torch.int16)),
+           torch.int16: (CG_DTYPE_F16, (torch.float16, torch.int16)),
+           torch.bfloat16: (CG_DTYPE_BF16, (torch.bfloat16,))}
 
+# The argument blocks are filled in one go: a single-token step costs a few
+# microseconds on the GPU, and setting 25 fields one by one as many here.
+_EXTEND = struct.Struct("@7i11P")
+_APPEND = struct.Struct("@9if3P3qPq7P")
+_ATTENTION = struct.Struct("@11if2P2q7PQ")
+assert (_EXTEND.size, _APPEND.size, _ATTENTION.size) == tuple(
+    map(ctypes.sizeof, (ExtendArgs, AppendArgs, AttentionArgs)))
 
-def _code(dtype: torch.dtype) -> int:
-    if dtype not in _DTYPES:
-        raise ValueError(f"dtype must be float16 (or int16 bits) or bfloat16, not {dtype}")
-    return _DTYPES[dtype]
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
 
 
 class _Call:
-    """Device, status word and launch of one object's calls."""
+    """Device, value type, status word and launch of one object's calls."""
 
-    def __init__(self, device, status):
+    def __init__(self, device, status, dtype: torch.dtype = torch.float16):
         self.device = torch.device(device)
         if self.device.type != "cuda":
             raise ValueError("the paged calls run on CUDA devices")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype must be float16 (or int16 bits) or bfloat16, not {dtype}")
+        self._index = self.device.index
+        self._code, self._dtypes = _DTYPES[dtype]
         self.status = (torch.zeros(1, dtype=torch.int32, device=self.device)
                        if status is None else status)
+        self._status = self._vector(self.status, "status", torch.int32, 1)
 
-    def _vector(self, t: torch.Tensor, name: str, dtype, count: int | None = None) -> int:
-        if t.dtype != dtype or t.device != self.device or not t.is_contiguous() or \
-                (count is not None and t.numel() < count):
+    def _vector(self, t: torch.Tensor, name: str, dtype, count: int = 0) -> int:
+        if t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous() or \
+                t.numel() < count:
             raise ValueError(f"{name} must be a contiguous {dtype} tensor on {self.device}"
-                             + (f" with at least {count} entries" if count is not None else ""))
+                             + (f" with at least {count} entries" if count else ""))
         return t.data_ptr()
 
-    def _rows(self, t: torch.Tensor, name: str, heads: int, dim: int, code: int) -> int:
-        """Token stride of [N, heads, dim] rows whose heads are contiguous."""
-        if t.device != self.device or _DTYPES.get(t.dtype) != code or t.dim() != 3 or \
-                t.shape[1] != heads or t.shape[2] != dim:
-            raise ValueError(f"{name} must be [N, {heads}, {dim}] of the object's type on "
+    def _rows(self, t: torch.Tensor, name: str, tokens: int, heads: int, dim: int) -> int:
+        """Token stride of [tokens, heads, dim] rows whose heads are contiguous."""
+        if t.dim() != 3 or t.shape != (tokens, heads, dim) or t.dtype not in self._dtypes or \
+                t.get_device() != self._index:
+            raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}] of the object's type on "
                              f"{self.device}")
         s0, s1, s2 = t.stride()
-        if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
+        if s2 != 1 or (s1 != dim and heads > 1):
             raise ValueError(f"{name}'s heads must be contiguous within a token")
-        return s0 if t.shape[0] > 1 else max(s0, heads * dim)
+        return s0 if tokens > 1 else max(s0, heads * dim)
 
-    def _pool(self, pool: torch.Tensor, shape: Shape, code: int) -> tuple[int, int]:
-        if pool.device != self.device or _DTYPES.get(pool.dtype) != code or pool.dim() != 6 or \
-                not pool.is_contiguous() or pool.shape[0] != shape.num_layers or \
-                pool.shape[1] != 2 or pool.shape[4] != shape.num_kv_heads or \
-                pool.shape[5] != shape.head_dim:
-            raise ValueError("pool must be a contiguous [L, 2, num_pages, page_tokens, H, D] "
-                             f"tensor of the object's type on {self.device}")
-        return pool.shape[2], pool.shape[3]
+    def _pool(self, pool: torch.Tensor, shape: Shape) -> tuple[int, int]:
+        if pool.dim() == 6:
+            layers, two, pages, page_tokens, heads, dim = pool.shape
+            if layers == shape.num_layers and two == 2 and heads == shape.num_kv_heads and \
+                    dim == shape.head_dim and pool.dtype in self._dtypes and \
+                    pool.get_device() == self._index and pool.is_contiguous():
+                return pages, page_tokens
+        raise ValueError("pool must be a contiguous [L, 2, num_pages, page_tokens, H, D] "
+                         f"tensor of the object's type on {self.device}")
 
     def _launch(self, fn, stream, *args) -> None:
         """fn(*args, stream) with this object's device current."""
         if stream is None:
-            handle = torch.cuda.current_stream(self.device).cuda_stream
+            handle = _raw_stream(self._index)
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
-        if torch.cuda.current_device() == self.device.index:
+        if _get_device() == self._index:
             rc = fn(*args, handle)
         else:
             with torch.cuda.device(self.device):
@@ -97,19 +110,15 @@ class PagedTables(_Call):
                  device, status: torch.Tensor | None = None):
         super().__init__(device, status)
         self.num_requests, self.max_tokens = num_requests, max_tokens
+        self.page_tokens, self.num_pages = page_tokens, num_pages
         dev = self.device
         self.kv_lens = torch.zeros(num_requests, dtype=torch.int32, device=dev)
         self.q_starts = torch.zeros(num_requests + 1, dtype=torch.int32, device=dev)
         self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=dev)
         self.positions = torch.full((max_tokens,), -1, dtype=torch.int32, device=dev)
         self.taken = torch.zeros(1, dtype=torch.int32, device=dev)
-        a = self._args = ExtendArgs()
-        a.num_requests, a.max_tokens = num_requests, max_tokens
-        a.page_tokens, a.num_pages = page_tokens, num_pages
-        a.kv_lens, a.q_starts = self.kv_lens.data_ptr(), self.q_starts.data_ptr()
-        a.slots, a.positions = self.slots.data_ptr(), self.positions.data_ptr()
-        a.taken_out, a.status = self.taken.data_ptr(), self.status.data_ptr()
-        self._ref = ctypes.byref(a)
+        self._args = ExtendArgs()
+        self._ref = ctypes.byref(self._args)
         self._fn = library().cg_extend_tables
 
     def extend(self, held: torch.Tensor, added: torch.Tensor, block_tables: torch.Tensor,
@@ -119,17 +128,18 @@ class PagedTables(_Call):
         block_tables: int32 [num_requests, max_pages], extended in place;
         free_pages: int32 page ids; taken: how many of them are handed out
         already (default: this object's own count)."""
-        a = self._args
-        if block_tables.dim() != 2 or block_tables.shape[0] != self.num_requests:
+        n = self.num_requests
+        if block_tables.dim() != 2 or block_tables.size(0) != n:
             raise ValueError("block_tables must be [num_requests, max_pages]")
-        a.held = self._vector(held, "held", torch.int32, self.num_requests)
-        a.added = self._vector(added, "added", torch.int32, self.num_requests)
-        a.block_tables = self._vector(block_tables, "block_tables", torch.int32)
-        a.max_pages = block_tables.shape[1]
-        a.free_pages = self._vector(free_pages, "free_pages", torch.int32)
-        a.num_free = free_pages.numel()
-        a.taken = self._vector(self.taken if taken is None else taken, "taken", torch.int32, 1)
-        a.position_base = position_base
+        i32, vector = torch.int32, self._vector
+        _EXTEND.pack_into(
+            self._args, 0, n, self.page_tokens, self.num_pages, block_tables.size(1),
+            free_pages.numel(), self.max_tokens, position_base, vector(held, "held", i32, n),
+            vector(added, "added", i32, n), vector(free_pages, "free_pages", i32),
+            vector(self.taken if taken is None else taken, "taken", i32, 1),
+            self.taken.data_ptr(), vector(block_tables, "block_tables", i32),
+            self.kv_lens.data_ptr(), self.q_starts.data_ptr(), self.slots.data_ptr(),
+            self.positions.data_ptr(), self._status)
         self._launch(self._fn, stream, self._ref)
 
 
@@ -147,13 +157,19 @@ class PagedAppend(_Call):
 
     def __init__(self, shape, num_q_heads: int, dtype: torch.dtype, device,
                  status: torch.Tensor | None = None):
-        super().__init__(device, status)
+        super().__init__(device, status, dtype)
         self.shape = shape if isinstance(shape, Shape) else Shape(*shape)
-        self.num_q_heads, self._type = num_q_heads, _code(dtype)
-        a = self._args = AppendArgs()
-        a.num_q_heads, a.dtype, a.status = num_q_heads, self._type, self.status.data_ptr()
-        self._refs = ctypes.byref(self.shape), ctypes.byref(a)
+        self.num_q_heads = num_q_heads
+        self._args = AppendArgs()
+        self._refs = ctypes.byref(self.shape), ctypes.byref(self._args)
         self._fn = library().cg_append_qkv
+
+    def _weight(self, w, name: str) -> int:
+        if w is None:
+            return 0
+        if w.dtype not in self._dtypes:
+            raise ValueError(f"{name} must be of the object's type")
+        return self._vector(w, name, w.dtype, self.shape.head_dim)
 
     def append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_out: torch.Tensor,
                pool: torch.Tensor, layer: int, positions: torch.Tensor | None,
@@ -163,34 +179,23 @@ class PagedAppend(_Call):
         q_out like q (or q itself); positions int32 [N] and slots int64 [N] as
         PagedTables makes them; rope: rope_table's, or None for no rotation;
         weights [D], or None for no norm."""
-        a, s, code = self._args, self.shape, self._type
-        n, h, d = q.shape[0], s.num_kv_heads, s.head_dim
-        a.q_stride = self._rows(q, "q", self.num_q_heads, d, code)
-        a.k_stride = self._rows(k, "k", h, d, code)
-        a.v_stride = self._rows(v, "v", h, d, code)
-        a.q_out_stride = self._rows(q_out, "q_out", self.num_q_heads, d, code)
-        if k.shape[0] != n or v.shape[0] != n or q_out.shape[0] != n:
-            raise ValueError("q, k, v and q_out must have the same number of tokens")
-        a.q, a.k, a.v, a.q_out = q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr()
-        a.num_tokens, a.layer = n, layer
-        a.num_pages, a.page_tokens = self._pool(pool, s, code)
-        a.pool = pool.data_ptr()
-        a.slots = self._vector(slots, "slots", torch.int64, n)
-        a.rot_dim = a.max_positions = 0
-        a.rope = a.positions = None
+        s, hq, rows = self.shape, self.num_q_heads, self._rows
+        n, h, d = q.size(0), s.num_kv_heads, s.head_dim
+        pages, page_tokens = self._pool(pool, s)
+        far = rot = table = where = 0
         if rope is not None:
-            if rope.dim() != 2:
-                raise ValueError("rope must be [max_positions, rot_dim]")
-            a.rope = self._vector(rope, "rope", torch.float32)
-            a.max_positions, a.rot_dim = rope.shape
-            a.positions = self._vector(positions, "positions", torch.int32, n)
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None:
-                if _DTYPES.get(w.dtype) != code:
-                    raise ValueError(f"{name} must be of the object's type")
-                self._vector(w, name, w.dtype, d)
-            setattr(a, name, None if w is None else w.data_ptr())
-        a.eps, a.interleaved = eps, int(interleaved)
+            if rope.dim() != 2 or positions is None:
+                raise ValueError("rope must be [max_positions, rot_dim], with positions")
+            far, rot = rope.shape
+            table = self._vector(rope, "rope", torch.float32)
+            where = self._vector(positions, "positions", torch.int32, n)
+        _APPEND.pack_into(
+            self._args, 0, n, hq, layer, pages, page_tokens, far, rot, int(interleaved),
+            self._code, eps, q.data_ptr(), k.data_ptr(), v.data_ptr(), rows(q, "q", n, hq, d),
+            rows(k, "k", n, h, d), rows(v, "v", n, h, d), q_out.data_ptr(),
+            rows(q_out, "q_out", n, hq, d), self._weight(q_weight, "q_weight"),
+            self._weight(k_weight, "k_weight"), table, where,
+            self._vector(slots, "slots", torch.int64, n), pool.data_ptr(), self._status)
         self._launch(self._fn, stream, *self._refs)
 
 
@@ -201,13 +206,12 @@ class PagedAttention(_Call):
 
     def __init__(self, shape, num_q_heads: int, dtype: torch.dtype, max_tokens: int,
                  max_requests: int, device, status: torch.Tensor | None = None):
-        super().__init__(device, status)
+        super().__init__(device, status, dtype)
         self.shape = shape if isinstance(shape, Shape) else Shape(*shape)
-        self.num_q_heads, self._type = num_q_heads, _code(dtype)
+        self.num_q_heads = num_q_heads
         self.max_tokens, self.max_requests = max_tokens, max_requests
-        a = self._args = AttentionArgs()
-        a.num_q_heads, a.dtype, a.status = num_q_heads, self._type, self.status.data_ptr()
-        self._refs = ctypes.byref(self.shape), ctypes.byref(a)
+        self._args = AttentionArgs()
+        self._refs = ctypes.byref(self.shape), ctypes.byref(self._args)
         self._fn, self._shared_fn = library().cg_attention_paged, library().cg_attention_shared
         self._scale = 1.0 / math.sqrt(self.shape.head_dim)
         self.workspace = None
@@ -218,8 +222,6 @@ class PagedAttention(_Call):
                                             self.max_requests, shared)
         if self.workspace is None or self.workspace.numel() < need:
             self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            self._args.workspace = self.workspace.data_ptr()
-            self._args.workspace_bytes = need
         self._has_shared = shared
 
     def reserve_shared(self) -> None:
@@ -228,28 +230,26 @@ class PagedAttention(_Call):
         if not self._has_shared:
             self._reserve(True)
 
-    def _set(self, q, pool, layer, q_starts, kv_lens, block_tables, max_q, out, scale, lse):
-        a, s, code = self._args, self.shape, self._type
-        n, requests = q.shape[0], kv_lens.numel()
+    def _set(self, q, pool, layer, q_starts, kv_lens, block_tables, max_q, out, window, sinks,
+             scale, lse):
+        s, hq = self.shape, self.num_q_heads
+        n, requests, d = q.size(0), kv_lens.numel(), s.head_dim
         if n > self.max_tokens or requests > self.max_requests:
             raise ValueError("more rows or requests than this object was made for")
-        a.q_stride = self._rows(q, "q", self.num_q_heads, s.head_dim, code)
-        a.out_stride = self._rows(out, "out", self.num_q_heads, s.head_dim, code)
-        if out.shape[0] != n:
-            raise ValueError("out must have as many rows as q")
-        if block_tables.dim() != 2 or block_tables.shape[0] != requests:
+        if block_tables.dim() != 2 or block_tables.size(0) != requests:
             raise ValueError("block_tables must be [num_requests, max_pages]")
-        a.q, a.out, a.num_tokens, a.num_requests = q.data_ptr(), out.data_ptr(), n, requests
-        a.max_q, a.layer = max_q, layer
-        a.num_pages, a.page_tokens = self._pool(pool, s, code)
-        a.pool = pool.data_ptr()
-        a.q_starts = self._vector(q_starts, "q_starts", torch.int32, requests + 1)
-        a.kv_lens = self._vector(kv_lens, "kv_lens", torch.int32)
-        a.block_tables = self._vector(block_tables, "block_tables", torch.int32)
-        a.max_pages = block_tables.shape[1]
-        a.scale = self._scale if scale is None else scale
-        a.lse = None if lse is None else self._vector(lse, "lse", torch.float32,
-                                                      n * self.num_q_heads)
+        pages, page_tokens = self._pool(pool, s)
+        i32, vector = torch.int32, self._vector
+        _ATTENTION.pack_into(
+            self._args, 0, requests, n, max_q, hq, layer, pages, page_tokens,
+            block_tables.size(1), window, sinks, self._code,
+            self._scale if scale is None else scale, q.data_ptr(), out.data_ptr(),
+            self._rows(q, "q", n, hq, d), self._rows(out, "out", n, hq, d),
+            0 if lse is None else vector(lse, "lse", torch.float32, n * hq),
+            vector(q_starts, "q_starts", i32, requests + 1), vector(kv_lens, "kv_lens", i32),
+            vector(block_tables, "block_tables", i32), pool.data_ptr(), self._status,
+            self.workspace.data_ptr(), self.workspace.numel())
+        return page_tokens
 
     def run(self, q: torch.Tensor, pool: torch.Tensor, layer: int, q_starts: torch.Tensor,
             kv_lens: torch.Tensor, block_tables: torch.Tensor, max_q: int, out: torch.Tensor,
@@ -259,8 +259,8 @@ class PagedAttention(_Call):
         block_tables int32 [B, max_pages] as PagedTables makes them; max_q: no
         request has more new tokens; window 0: no window; scale: 1 / sqrt(D)
         by default; lse: fp32 [N, Hq] that receives the log-sums."""
-        self._set(q, pool, layer, q_starts, kv_lens, block_tables, max_q, out, scale, lse)
-        self._args.window, self._args.sinks = window, sinks
+        self._set(q, pool, layer, q_starts, kv_lens, block_tables, max_q, out, window, sinks,
+                  scale, lse)
         self._launch(self._fn, stream, *self._refs)
         return out
 
@@ -272,10 +272,9 @@ class PagedAttention(_Call):
         """As run without a window, behind a prefix of prefix_tokens tokens in
         the pages of prefix_table (int32) that every request shares."""
         self.reserve_shared()
-        self._set(q, pool, layer, q_starts, kv_lens, block_tables, max_q, out, scale, lse)
-        a = self._args
-        pages = -(-prefix_tokens // a.page_tokens)
-        table = self._vector(prefix_table, "prefix_table", torch.int32, pages)
-        a.window = a.sinks = 0
+        page_tokens = self._set(q, pool, layer, q_starts, kv_lens, block_tables, max_q, out, 0, 0,
+                                scale, lse)
+        table = self._vector(prefix_table, "prefix_table", torch.int32,
+                             -(-prefix_tokens // page_tokens))
         self._launch(self._shared_fn, stream, *self._refs, table, prefix_tokens)
         return out
