@@ -16,7 +16,8 @@
 namespace cg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int64_t kResident = 148 * 2048;  // threads of all SMs
 
 __global__ void rope_kernel(int32_t max_positions, int32_t half, double theta, float* out) {
   const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -40,76 +41,108 @@ struct AppendParams {
   int64_t num_tokens, num_slots;
   float eps;
   int max_positions, rot, interleaved, q_heads, kv_heads, dim;
-  int units;  // head groups of a token
+  int units;    // head groups of a token
+  int by_four;  // a lane's four angles of a row of the table lie on 16 bytes
   int32_t* status;
+};
+
+// Large calls (several heads a group) go past the cache: their values are read
+// once, and what they write is more than stays there.
+template <int HEADS>
+__device__ __forceinline__ uint4 load(const uint16_t* p) {
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  return HEADS > 1 ? __ldcs(q) : *q;
+}
+template <int HEADS>
+__device__ __forceinline__ void store(uint16_t* p, uint4 v) {
+  if (HEADS > 1) __stcs(reinterpret_cast<uint4*>(p), v);
+  else *reinterpret_cast<uint4*>(p) = v;
+}
+
+// How a lane comes by the partners and angles of its values.
+enum Turn {
+  kNone,         // no rotation
+  kHalves,       // rot/2 apart, a multiple of eight: the partners are in another lane
+  kInterleaved,  // next to each other
+  kScattered     // any other: partners are read again, from L1
 };
 
 // LANES: lanes of a head's vector (a power of two >= dim / 8).  HEADS: heads a
 // group of lanes takes at a time, all of one token.
-template <typename T, int LANES, int HEADS>
+template <typename T, int LANES, int HEADS, Turn TURN>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
   const int64_t group = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / LANES;
   const int lane = threadIdx.x % LANES;
   const int64_t t = group / p.units;
   const int e0 = lane * 8;
-  int64_t slot = -1;
-  int pos = 0;
-  if (t < p.num_tokens) {
-    slot = p.slots[t];
-    if (p.rot > 0) pos = p.positions[t];
-    // a bad row is left out whole; only a negative slot is one on purpose
-    if (slot >= 0 &&
-        (slot >= p.num_slots || (p.rot > 0 && (pos < 0 || pos >= p.max_positions)))) {
-      if (lane == 0) report(p.status, CG_ERR_MISMATCH);
-      slot = -1;
-    }
-  }
-  const bool live = slot >= 0 && e0 < p.dim;
   const int head0 = int(group - t * p.units) * HEADS;
   const int heads = p.q_heads + 2 * p.kv_heads;
   const int first_v = p.q_heads + p.kv_heads;
+  const bool have = t < p.num_tokens && e0 < p.dim;
 
+  // the values first: nothing decides whether they can be read
   const uint16_t* src[HEADS];
-  uint16_t* dst[HEADS];
   uint4 raw[HEADS];
 #pragma unroll
   for (int u = 0; u < HEADS; ++u) {
     const int h = head0 + u;
-    src[u] = nullptr;
-    dst[u] = nullptr;
     raw[u] = make_uint4(0, 0, 0, 0);
-    if (!live || h >= heads) continue;
-    if (h < p.q_heads) {
-      src[u] = p.q + t * p.q_stride + int64_t(h) * p.dim;
-      dst[u] = p.q_out + t * p.q_out_stride + int64_t(h) * p.dim;
-    } else {
-      const int k = h < first_v ? h - p.q_heads : h - first_v;
-      src[u] = (h < first_v ? p.k + t * p.k_stride : p.v + t * p.v_stride) + int64_t(k) * p.dim;
-      dst[u] = (h < first_v ? p.k_pool : p.v_pool) + (slot * p.kv_heads + k) * int64_t(p.dim);
-    }
-    raw[u] = *reinterpret_cast<const uint4*>(src[u] + e0);
+    src[u] = h < p.q_heads  ? p.q + t * p.q_stride + int64_t(h) * p.dim
+             : h < first_v ? p.k + t * p.k_stride + int64_t(h - p.q_heads) * p.dim
+                           : p.v + t * p.v_stride + int64_t(h - first_v) * p.dim;
+    if (have && h < heads) raw[u] = load<HEADS>(src[u] + e0);
   }
+  int64_t slot = -1;
+  int pos = 0;
+  if (t < p.num_tokens) {
+    slot = p.slots[t];
+    if (TURN != kNone) pos = p.positions[t];
+    // a bad row is left out whole; only a negative slot is one on purpose
+    if (slot >= 0 &&
+        (slot >= p.num_slots || (TURN != kNone && (pos < 0 || pos >= p.max_positions)))) {
+      if (lane == 0) report(p.status, CG_ERR_MISMATCH);
+      slot = -1;
+    }
+  }
+  const bool live = have && slot >= 0;
 
-  // The pair and angle of each of the lane's eight values.  Pairs next to each
-  // other are in the lane; pairs rot/2 apart are lane_step lanes away where
-  // rot/2 is a multiple of eight, and are read again from memory (L1) otherwise.
   const int half = p.rot / 2;
-  const bool turn = e0 < p.rot;
-  const bool by_lane = !p.interleaved && half % 8 == 0;
-  const int partner = by_lane ? (e0 < half ? lane + half / 8 : lane - half / 8) : lane;
-  float co[8], si[8];
+  const bool turn = TURN != kNone && e0 < p.rot;
+  const int partner = e0 < half ? lane + half / 8 : lane - half / 8;  // kHalves
+  float co[8], si[8];  // y <- y co + partner si
+  if (TURN != kNone) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) co[i] = 1.f, si[i] = 0.f;
-  if (live && turn && head0 < first_v) {
-    const float* row = p.rope + int64_t(pos) * p.rot;
+    for (int i = 0; i < 8; ++i) co[i] = 1.f, si[i] = 0.f;
+    if (live && turn && head0 < first_v) {
+      const float* row = p.rope + int64_t(pos) * p.rot;
+      if (TURN == kHalves) {
+        const float4* c = reinterpret_cast<const float4*>(row + (e0 < half ? e0 : e0 - half));
+        const float4* s = reinterpret_cast<const float4*>(row + (e0 < half ? e0 + half : e0));
+        const float sign = e0 < half ? -1.f : 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = e0 + i;
-      if (e < p.rot) {
-        const int a = p.interleaved ? e >> 1 : (e < half ? e : e - half);
-        co[i] = __ldg(row + a);
-        si[i] = __ldg(row + half + a);
-        if (p.interleaved ? !(e & 1) : e < half) si[i] = -si[i];  // y_a c - y_b s
+        for (int i = 0; i < 2; ++i) {
+          const float4 a = __ldg(c + i), b = __ldg(s + i);
+          co[4 * i] = a.x, co[4 * i + 1] = a.y, co[4 * i + 2] = a.z, co[4 * i + 3] = a.w;
+          si[4 * i] = sign * b.x, si[4 * i + 1] = sign * b.y;
+          si[4 * i + 2] = sign * b.z, si[4 * i + 3] = sign * b.w;
+        }
+      } else if (TURN == kInterleaved && p.by_four) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(row + e0 / 2));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + e0 / 2));
+        co[0] = co[1] = a.x, co[2] = co[3] = a.y, co[4] = co[5] = a.z, co[6] = co[7] = a.w;
+        si[0] = -b.x, si[1] = b.x, si[2] = -b.y, si[3] = b.y;
+        si[4] = -b.z, si[5] = b.z, si[6] = -b.w, si[7] = b.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = e0 + i;
+          if (e < p.rot) {
+            const int a = p.interleaved ? e >> 1 : (e < half ? e : e - half);
+            co[i] = __ldg(row + a);
+            si[i] = __ldg(row + half + a);
+            if (p.interleaved ? !(e & 1) : e < half) si[i] = -si[i];  // y_a c - y_b s
+          }
+        }
       }
     }
   }
@@ -148,12 +181,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
         }
       }
     }
-    if (p.rot > 0) {
+    if (TURN != kNone) {
       float z[8];
-      if (p.interleaved) {
+      if (TURN == kInterleaved) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = y[i ^ 1];
-      } else if (by_lane) {
+      } else if (TURN == kHalves) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = __shfl_sync(group_mask, y[i], partner, LANES);
       } else {
@@ -177,13 +210,21 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
     raw[u] = make_uint4(T::pack(y[0], y[1]), T::pack(y[2], y[3]), T::pack(y[4], y[5]),
                         T::pack(y[6], y[7]));
   }
+  if (!live) return;
 #pragma unroll
-  for (int u = 0; u < HEADS; ++u)
-    if (dst[u] != nullptr) *reinterpret_cast<uint4*>(dst[u] + e0) = raw[u];
+  for (int u = 0; u < HEADS; ++u) {
+    const int h = head0 + u;
+    if (h >= heads) break;
+    uint16_t* dst =
+        h < p.q_heads ? p.q_out + t * p.q_out_stride + int64_t(h) * p.dim
+        : h < first_v ? p.k_pool + (slot * p.kv_heads + h - p.q_heads) * int64_t(p.dim)
+                      : p.v_pool + (slot * p.kv_heads + h - first_v) * int64_t(p.dim);
+    store<HEADS>(dst + e0, raw[u]);
+  }
 }
 
-template <typename T, int LANES>
-cudaError_t launch_lanes(AppendParams& p, cudaStream_t stream) {
+template <typename T, int LANES, Turn TURN>
+cudaError_t launch_turn(AppendParams& p, cudaStream_t stream) {
   const int heads = p.q_heads + 2 * p.kv_heads;
   const auto go = [&](auto kernel, int per) {
     p.units = (heads + per - 1) / per;
@@ -191,7 +232,23 @@ cudaError_t launch_lanes(AppendParams& p, cudaStream_t stream) {
     kernel<<<unsigned((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
   };
-  return go(append_kernel<T, LANES, 4>, 4);
+  // One head a group while the machine holds all groups at once: nothing hides
+  // a group's latency then but its own shortness.  Four beyond, whose loads are
+  // on their way together and share the token's angles.  64 tokens of 48 heads
+  // of 128: 2.7 us and 4.0; 10,752 tokens of 96: 167 us and 92.
+  if (p.num_tokens * heads * LANES <= kResident)
+    return go(append_kernel<T, LANES, 1, TURN>, 1);
+  return go(append_kernel<T, LANES, 4, TURN>, 4);
+}
+
+template <typename T, int LANES>
+cudaError_t launch_lanes(AppendParams& p, cudaStream_t stream) {
+  if (p.rot == 0) return launch_turn<T, LANES, kNone>(p, stream);
+  if (p.interleaved) return launch_turn<T, LANES, kInterleaved>(p, stream);
+  // the table's rows are read 16 bytes at a time
+  if (p.rot % 16 == 0 && p.by_four)
+    return launch_turn<T, LANES, kHalves>(p, stream);
+  return launch_turn<T, LANES, kScattered>(p, stream);
 }
 
 template <typename T>
@@ -228,6 +285,7 @@ cudaError_t launch_append(const cg_append_args& a, const cg_shape& s, cudaStream
   p.eps = a.eps;
   p.rope = a.rope_dev;
   p.max_positions = a.max_positions;
+  p.by_four = a.rot_dim % 8 == 0 && (reinterpret_cast<uintptr_t>(a.rope_dev) & 15) == 0;
   p.rot = a.rot_dim;
   p.interleaved = a.interleaved;
   p.positions = a.positions_dev;
