@@ -8,7 +8,8 @@
 namespace cg {
 namespace {
 
-constexpr int kMaxCtas = 160;  // of either kernel, one an SM
+constexpr int kMaxCtas = 160;  // of the tile kernel, one an SM
+constexpr int kMaxRowCtas = kMaxCtas * kRowCtasPerSm;
 constexpr int64_t kInStepBytes = 64 << 20;  // half of the L2 cache
 
 // Block 0 sums up the rows kernel's line, block 1 the tile kernel's.
@@ -208,9 +209,9 @@ Workspace workspace_of(const cg_shape& s, int Hq, int tokens, int requests, bool
     return here;
   };
   w.row_cum = take((row_slots + 1) * 8);
-  w.row_cuts = take(kMaxCtas * sizeof(Cut));
-  w.row_pieces = take(uint64_t(2) * kMaxCtas * kRowTile * D * 4);
-  w.row_stats = take(uint64_t(2) * kMaxCtas * kRowTile * 8);
+  w.row_cuts = take(kMaxRowCtas * sizeof(Cut));
+  w.row_pieces = take(uint64_t(2) * kMaxRowCtas * kRowTile * D * 4);
+  w.row_stats = take(uint64_t(2) * kMaxRowCtas * kRowTile * 8);
   w.tile_cum = take((tile_slots + 1) * 8);
   w.tile_cuts = take(tile_ctas * sizeof(Cut));
   w.tile_pieces = take(2 * tile_ctas * tile * D * 4);
@@ -223,7 +224,7 @@ Workspace workspace_of(const cg_shape& s, int Hq, int tokens, int requests, bool
 
 template <typename T, int kTile, int kKeys>
 cudaError_t launch_all(AttnParams& p, int sms, cudaStream_t stream) {
-  p.rows.ctas = std::min(kMaxCtas, sms);
+  p.rows.ctas = std::min(kMaxRowCtas, sms * kRowCtasPerSm);
   p.rows.tile = kRowTile;
   const bool tiles = p.tiled || (p.shared && !p.prefix_small);
   p.tiles.ctas = tiles ? std::min(kMaxCtas, sms) : 0;

@@ -29,7 +29,8 @@
 namespace cg {
 
 constexpr int kRowTile = 16;   // query rows of an item of the rows kernel (one matrix tile)
-constexpr int kRowKeys = 128;  // keys of a unit there
+constexpr int kRowKeys = 64;   // keys of a unit there
+constexpr int kRowCtasPerSm = 2;
 constexpr int kScanSlots = 1024;  // slots of a line that every CTA sums up by itself
 
 // The line of work of one of the two kernels, in the workspace.
@@ -170,7 +171,7 @@ __device__ __forceinline__ int slot_base(const AttnParams& p, int r) {
 // units, so that shares of many short items are not longer than others.
 template <int kTile>
 __host__ __device__ constexpr int item_cost() {
-  return kTile == kRowTile ? 1 : 2;
+  return kTile == kRowTile ? 1 : 4;
 }
 
 // The item of slot x and its units for each kv head; 0 where it holds no rows.

@@ -5,9 +5,10 @@
 //
 // in one pass over the keys with a running maximum m.  A row of K and V serves
 // at most 16 query rows, so the bytes of K and V bound it, and all that counts
-// is that enough of them are on their way: one CTA an SM, whose ring of stages
-// (kv_loader.cuh) takes most of the shared memory, about 190 KB.  Eight warps
-// read the stages, 16 keys of each unit a warp, with the matrix instructions of
+// is that enough of them are on their way: two CTAs an SM, whose rings of stages
+// (kv_loader.cuh) take most of the shared memory, 96 KB each; while one is at the
+// end of an item the other reads on.  Four warps read a CTA's
+// stages, 16 keys of each unit a warp, with the matrix instructions of
 // a warp (the tensor-memory products want 128 rows).  The keys, and then the
 // channels, are the 16 rows of those, the query rows their 8 columns,
 //     S^T = K Q^T,   O^T = V^T P^T,
@@ -23,16 +24,16 @@
 namespace cg {
 namespace {
 
-constexpr int kWarps = 8;  // that compute
+constexpr int kWarps = 4;  // that compute
 constexpr int kThreads = 32 * (kWarps + kLoadWarps);
-constexpr int kJoinBytes = 17 * 1024;
+constexpr int kJoinBytes = 8704;
 constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
 static_assert(kRowKeys == 16 * kWarps, "each warp takes 16 keys of a unit");
 static_assert(kJoinBytes >= (kScanSlots + 1) * 8, "the line's sums lie there at first");
 
 template <int DC>
 struct Shape {
-  static constexpr int kStages = DC == 4 ? 3 : (DC == 2 ? 6 : 8);
+  static constexpr int kStages = DC == 4 ? 3 : (DC == 2 ? 6 : 12);
   static constexpr int kStage = DC * kRowKeys * 128;
   // a row of a warp's output for the join: four channels more, so that the four
   // rows that a store touches fall on different banks
@@ -66,7 +67,7 @@ __device__ __forceinline__ void compute_sync() {
 
 // NR: products of eight query rows, 1 or 2.
 template <typename T, int DC, int NR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
     rows_kernel(AttnParams p, const __grid_constant__ KvMaps maps) {
   using S = Shape<DC>;
   extern __shared__ uint8_t smem_raw[];
@@ -81,6 +82,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ring ring{base, smem_addr(bars), smem_addr(bars) + 8 * S::kStages, no_page, &dead_mem};
 
   let_next_start();
+  if (threadIdx.x == 32 * kWarps && maps.box > 0) {
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+  }
   if (threadIdx.x == 0) {
     dead_mem = 0;
     for (int i = 0; i < S::kStages; ++i) {

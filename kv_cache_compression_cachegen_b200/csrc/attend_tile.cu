@@ -189,6 +189,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   bar.item_free = bar.item_full + 8 * kItems;
 
   let_next_start();
+  if (threadIdx.x == 32 * kLoadWarp && maps.box > 0) {
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+  }
+  if (threadIdx.x == 32 * kQueryWarp && by_map) prefetch_map(&q_map);
   if (threadIdx.x == 0) {
     dead_mem = 0;
     for (int i = 0; i < G::kStages; ++i) {

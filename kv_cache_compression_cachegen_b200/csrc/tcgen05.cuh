@@ -81,6 +81,9 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
       "r"(bytes)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // A box of a tensor map to shared memory; by any thread.
 __device__ __forceinline__ void tma_load3_own(uint32_t dst, const void* map, int x, int y, int z,
                                               uint32_t bar) {
