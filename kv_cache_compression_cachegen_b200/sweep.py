@@ -20,6 +20,10 @@ llama34b   the Llama-34B shape: first the three-level pre-encode of a
 paged      the Llama-2-7B shape (balanced) decoded into a paged pool of
            16-token pages through a shuffled block table, against the flat
            cg_decode_into of the same containers (and checked equal to it).
+serve      the Llama-2-7B shape (balanced) decoded into a paged pool as the
+           document that a batch of 64 requests shares, and then one step of
+           the batch behind it: block tables and slot map, and for one layer
+           the append of the new tokens and the attention behind the document.
 formats    format 1 (deltas to the group's anchor) against format 2 (deltas
            between adjacent tokens): compression ratio and encode / decode
            GB/s of both on the Llama-2-7B shape (balanced), the Mistral-7B
@@ -282,9 +286,76 @@ def run_streamed(dev, warmup, reps):
                       "h2d_gbps_during_stream": round(comp_bytes / ms_s / 1e6, 1)}), flush=True)
 
 
+def run_serve(dev, warmup, reps, requests=64, held=300, page_tokens=16):
+    """A document decoded from its containers into the pool, and a batch behind it."""
+    w = synth.WORKLOADS["llama2_7b"]
+    kv = _gen(w, dev)
+    shape = Shape(w.L, w.H, w.D)
+    stream = torch.cuda.current_stream(dev)
+    enc = ta.encode(kv, w.C, 1)
+    ta.raise_on_status(enc.status, "cg_encode")
+    doc = w.T
+    doc_pages = -(-doc // page_tokens)
+    own_pages = -(-(held + 1) // page_tokens)
+    pages = doc_pages + requests * own_pages
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(0))
+    order = order.to(torch.int32).to(dev)
+    table, free = order[:doc_pages].contiguous(), order[doc_pages:].contiguous()
+    pool = torch.empty((w.L, 2, pages, page_tokens, w.H, w.D), dtype=torch.float16, device=dev)
+    status = ta.new_status(dev)
+    ms_doc = _time(lambda: ta.decode_into_paged(enc.data, enc.stride, shape, w.C, 1, w.num_chunks,
+                                                pool, page_tokens, table, doc, status,
+                                                stream=stream), stream, warmup, reps)
+    tables = ta.PagedTables(requests, requests * held, page_tokens, pages, dev, status)
+    append = ta.PagedAppend(shape, w.H, torch.float16, dev, status)
+    attend = ta.PagedAttention(shape, w.H, torch.float16, requests * held, requests, dev, status)
+    attend.reserve_shared()
+    rope = ta.rope_table(doc + held + 1, w.D, dev)
+    bt = torch.full((requests, own_pages), -1, dtype=torch.int32, device=dev)
+    gen = torch.Generator(device=dev).manual_seed(1)
+
+    def tokens(n):
+        return torch.randn((n, 3 * w.H, w.D), generator=gen, device=dev).to(torch.float16)
+
+    def add(n):
+        return torch.full((requests,), n, dtype=torch.int32, device=dev)
+    h = w.H
+    # what the batch has asked so far
+    qkv = tokens(requests * held)
+    tables.extend(tables.kv_lens, add(held), bt, free, position_base=doc)
+    append.append(qkv[:, :h], qkv[:, h:2 * h], qkv[:, 2 * h:], qkv[:, :h], pool, 0,
+                  tables.positions, tables.slots, rope)
+    # one more token each: the lengths stay, so that every repetition is the same step
+    step = ta.PagedTables(requests, requests, page_tokens, pages, dev, status)
+    one, held_now, taken = add(1), tables.kv_lens.clone(), tables.taken.clone()
+    qkv = tokens(requests)
+    q_out, out = (torch.empty((requests, h, w.D), dtype=torch.float16, device=dev)
+                  for _ in range(2))
+
+    def extend():
+        step.extend(held_now, one, bt, free, taken, position_base=doc)
+
+    def store():
+        append.append(qkv[:, :h], qkv[:, h:2 * h], qkv[:, 2 * h:], q_out, pool, 0, step.positions,
+                      step.slots, rope)
+
+    def answer():
+        attend.run_shared(q_out, pool, 0, table, doc, step.q_starts, step.kv_lens, bt, 1, out)
+    us = {name: 1e3 * _time(fn, stream, warmup, reps)
+          for name, fn in (("extend", extend), ("append", store), ("attend", answer))}
+    ta.raise_on_status(status, "serve")
+    if not bool(torch.isfinite(out).all()):
+        raise RuntimeError("attention output is not finite")
+    print(json.dumps({"workload": "llama2_7b", "serve": True, "requests": requests,
+                      "document_tokens": doc, "own_tokens": held + 1,
+                      "page_tokens": page_tokens, "decode_document_ms": round(ms_doc, 3),
+                      **{f"{k}_us": round(v, 2) for k, v in us.items()}}), flush=True)
+
+
 def main() -> int:
     ap = argparse.ArgumentParser()
-    ap.add_argument("--config", choices=["mistral7b", "sweep", "llama34b", "formats", "paged"],
+    ap.add_argument("--config", choices=["mistral7b", "sweep", "llama34b", "formats", "paged",
+                                         "serve"],
                     required=True)
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--reps", type=int, default=5)
@@ -301,6 +372,8 @@ def main() -> int:
         run_formats(dev, args.warmup, args.reps)
     elif args.config == "paged":
         run_paged(dev, args.warmup, args.reps)
+    elif args.config == "serve":
+        run_serve(dev, args.warmup, args.reps)
     else:
         run_preencode(dev, args.warmup, args.reps)
         run_streamed(dev, args.warmup, args.reps)
