@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
   using S = Shape<DC>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[2 * S::kStages];
-  __shared__ uint32_t no_page[4][4];
+  __shared__ uint32_t no_page[kNoted][4];
   __shared__ int dead_mem;
   __shared__ float stat_m[kWarps][16], stat_l[kWarps][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
           for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[n][e] = half[0][n][e] + half[1][n][e];
-          holes = (no_page[unit_count & 3][warp >> 1] >> (16 * (warp & 1))) & 0xFFFFu;
+          holes = (no_page[unit_count % kNoted][warp >> 1] >> (16 * (warp & 1))) & 0xFFFFu;
         }
         release();
         bool full = true, mixed = false;

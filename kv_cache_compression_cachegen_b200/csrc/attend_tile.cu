@@ -33,6 +33,11 @@ struct Geometry {
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kKeys = DC <= 2 ? 128 : 64;    // keys of a unit
   static constexpr int kStages = 4;                   // K and V tiles in flight
+  // Pairs j of weights with (j & kPolynomial) == 8 go to exp2_pair.  With up to 64
+  // channels the exponentials bound the kernel, and an eighth of them there made
+  // two prompts of 8,192 tokens 835 us (none: 889, a quarter: 859); with 128 a
+  // sixteenth 1,042 (none: 1,105, a quarter: 1,154).
+  static constexpr int kPolynomial = DC == 1 ? 15 : 31;
   static constexpr int kQBytes = 128 * 128;           // a 64-channel block of a query tile
   static constexpr int kBlock = kKeys * 128;          // a 64-channel block of a K or V tile
   static constexpr int kStage = DC * kBlock;
@@ -67,14 +72,12 @@ struct Deal {
   int head, piece, whole;
 };
 
-// 2^x of two values without the special-function unit, for the eighth of a
-// unit's weights that the multiply-add pipe has time for: n = round(x) by adding
+// 2^x of two values without the special-function unit, for the few of a unit's
+// weights that the multiply-add pipe has time for: n = round(x) by adding
 // 1.5 * 2^23, a polynomial for 2^(x - n) on [-1/2, 1/2], n added to the exponent.
 // The coefficients are the minimax ones of degree 5 for the relative error (Remez
 // exchange), 2^-23.7, and 2^-22 as evaluated in fp32 -- what ex2.approx has.
-// Below -125 the result stays 2^-125.  (Of a unit's 128 weights a row, none to
-// three eighths were tried: an eighth is as fast as a quarter or faster
-// everywhere, and a tenth faster than none on short items.)
+// Below -125 the result stays 2^-125.
 __device__ __forceinline__ float2 exp2_pair(float2 x) {
   const float2 magic = make_float2(12582912.f, 12582912.f);
   const float2 minus = make_float2(-12582912.f, -12582912.f);
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Deal deals[kItems];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_mem;
-  __shared__ __align__(16) uint32_t no_page[4][4];
+  __shared__ __align__(16) uint32_t no_page[kNoted][4];
   const int warp = __shfl_sync(~0u, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t q_smem = base;
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_wait(bar.s_full + 8 * tile, s_phase, dead))) break;
         s_phase ^= 1;
         tc_fence_after();
-        const uint4 hole = *reinterpret_cast<const uint4*>(no_page[unit_count & 3]);
+        const uint4 hole = *reinterpret_cast<const uint4*>(no_page[unit_count % kNoted]);
         uint32_t raw[G::kKeys];
         tmem_load<G::kKeys>(t_s, raw);
         if (!full || (hole.x | hole.y | hole.z | hole.w) != 0) {
@@ -316,9 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = h * (G::kKeys / 2); j < (h + 1) * (G::kKeys / 2); j += 2) {
             const float2 x = fma_pair(
                 make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])), scale2, shift2);
-            // a sixteenth on the multiply-add pipe: see exp2_pair
-            const float2 e = (j & 31) == 8 ? exp2_pair(x)
-                                           : make_float2(exp2_fast(x.x), exp2_fast(x.y));
+            // a few on the multiply-add pipe: see exp2_pair
+            const float2 e = (j & G::kPolynomial) == 8
+                                 ? exp2_pair(x)
+                                 : make_float2(exp2_fast(x.x), exp2_fast(x.y));
             sum[(j >> 1) & 1] = add_pair(sum[(j >> 1) & 1], e);
             // rounded to the pool's type for the product with V: half a step of it
             // relative to each weight; the sum is not

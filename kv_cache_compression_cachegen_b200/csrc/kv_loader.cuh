@@ -18,12 +18,15 @@
 namespace cg {
 
 constexpr int kLoadWarps = 2;
+constexpr uint32_t kNoted = 8;
 
 // The ring, as both sides see it.
 struct Ring {
   uint32_t smem;         // stage 0
   uint32_t full, empty;  // barriers, 8 bytes a stage
-  // keys of a unit whose page is not in the pool, a bit each, by unit number mod 4
+  // Keys of a unit whose page is not in the pool, a bit each, by unit number mod
+  // kNoted: a unit's note is written over when the stage of the unit kNoted behind
+  // it is free, which at up to twelve stages is after the unit was read.
   uint32_t (*no_page)[4];
   volatile int* dead;
 };
@@ -34,6 +37,7 @@ template <int DC, int kTile, int kKeys, int kStages>
 __device__ __forceinline__ bool load_kv(const AttnParams& p, Walk<kTile, kKeys>& w,
                                         const Ring& ring, const CUtensorMap* k_map,
                                         const CUtensorMap* v_map, int box, int wk) {
+  static_assert(kStages / 2 + 1 <= int(kNoted), "");
   constexpr int kBlock = kKeys * 128, kStage = DC * kBlock;
   constexpr int kMine = kKeys / kLoadWarps;  // rows of a tile that are this warp's
   constexpr int kOwn = kMine / 32;           // of these, a lane's
@@ -108,7 +112,7 @@ __device__ __forceinline__ bool load_kv(const AttnParams& p, Walk<kTile, kKeys>&
         ok = __all_sync(~0u, mbar_wait(ring.empty + 8 * stage, phase, ring.dead));
         if (!ok) break;
         if (kv == 0 && lane < kOwn)
-          ring.no_page[unit_count & 3][wk * kOwn + lane] = lane == 0 ? holes[0] : holes[kOwn - 1];
+          ring.no_page[unit_count % kNoted][wk * kOwn + lane] = lane == 0 ? holes[0] : holes[kOwn - 1];
         const uint32_t tile = ring.smem + stage * kStage;
         if (there) {
           // whole boxes of keys that follow one another in a page
@@ -161,6 +165,7 @@ template <int DC, int kTile, int kKeys, int kStages>
 __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKeys>& w,
                                            const Ring& ring, const CUtensorMap* k_map,
                                            const CUtensorMap* v_map, int box, int wk) {
+  static_assert(kStages / 2 + 1 <= int(kNoted), "");
   constexpr int kBlock = kKeys * 128, kStage = DC * kBlock;
   constexpr int kMine = kKeys / kLoadWarps;
   static_assert(kMine / 8 <= 32 && kMine <= 64, "a lane has at most one box's keys");
@@ -215,7 +220,7 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
     for (int kv = 0; kv < 2; ++kv) {
       if (!__all_sync(~0u, mbar_wait(ring.empty + 8 * stage, phase, ring.dead))) return false;
       if (kv == 0 && lane < kMine / 32)
-        ring.no_page[unit_count & 3][wk * (kMine / 32) + lane] = holes[lane & 1];
+        ring.no_page[unit_count % kNoted][wk * (kMine / 32) + lane] = holes[lane & 1];
       __syncwarp();
       mbar_expect(ring.full + 8 * stage, __popc(there) * box * (128 * DC));
       const uint32_t dst = ring.smem + stage * kStage + kMine * wk * 128;

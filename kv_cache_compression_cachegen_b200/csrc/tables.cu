@@ -44,6 +44,16 @@ __device__ __forceinline__ int pages_of(int n, const FastDiv& div) {
   return q + (n != q * int(div.d));
 }
 
+// The first request from lo to hi whose inclusive sum passes t (hi's does).
+__device__ __forceinline__ int request_behind(const int32_t* end, int lo, int hi, int t) {
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
 // Give every CTA of the cluster the first code (in rank order) that any of them found.
 __device__ int32_t cluster_first(int32_t mine, int32_t* slots, int rank, int size) {
   if (threadIdx.x < size) {
@@ -59,6 +69,8 @@ __device__ int32_t cluster_first(int32_t mine, int32_t* slots, int rank, int siz
   return all;
 }
 
+// kPer: tokens of a thread at a time.
+template <int kPer>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(cg_extend_args a, FastDiv div) {
   extern __shared__ int32_t smem[];
   const int B = a.num_requests;
@@ -174,54 +186,58 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(cg_extend_args a, F
     a.q_starts_dev[r + 1] = end;
   }
   // A token in its request's partly filled last page reads that page's table
-  // entry, which no thread writes; all others take their page from the free list.
-  for (int t = first; t < a.max_tokens; t += step) {
-    int64_t slot = -1;
-    int32_t pos = -1;
-    if (t < total) {
-      int lo = 0, hi = B - 1;  // the first request whose range ends behind t
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (tok_end[mid] > t) hi = mid;
-        else lo = mid + 1;
-      }
-      const int at = held_s[lo] + t - (lo ? tok_end[lo - 1] : 0);
-      const int col = div_of(at, div);
-      const int have = pages_of(held_s[lo], div);
-      const int32_t page =
-          col < have ? a.block_tables_dev[(long long)lo * a.max_pages + col]
-                     : a.free_pages_dev[taken + (lo ? page_end[lo - 1] : 0) + (col - have)];
-      slot = int64_t(page) * P + (at - col * P);
-      pos = a.position_base + at;
+  // entry, which no thread writes; all others take their page from the free
+  // list.  A warp takes kPer * 32 tokens that follow one another and looks for
+  // the requests of the first and the last: where those are one, no lane has to
+  // search.  Their pages' entries are asked for together.
+  constexpr int kChunk = 32 * kPer;
+  for (int64_t c0 = int64_t(first >> 5) * kChunk; c0 < a.max_tokens; c0 += int64_t(step) * kPer) {
+    int r0 = 0, r1 = B - 1;
+    if (kPer > 1 && c0 < total) {
+      r0 = request_behind(tok_end, 0, B - 1, int(c0));
+      r1 = request_behind(tok_end, r0, B - 1, int(min(c0 + kChunk - 1, int64_t(total) - 1)));
     }
-    a.slots_dev[t] = slot;
-    a.positions_dev[t] = pos;
+    int32_t page[kPer], row[kPer], pos[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t t = c0 + 32 * i + lane;
+      page[i] = row[i] = 0;
+      pos[i] = -1;
+      if (t < total) {
+        const int r = request_behind(tok_end, r0, r1, int(t));
+        const int at = held_s[r] + int(t) - (r ? tok_end[r - 1] : 0);
+        const int col = div_of(at, div), have = pages_of(held_s[r], div);
+        page[i] = *(col < have
+                        ? a.block_tables_dev + (long long)r * a.max_pages + col
+                        : a.free_pages_dev + taken + (r ? page_end[r - 1] : 0) + (col - have));
+        row[i] = at - col * P;
+        pos[i] = a.position_base + at;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t t = c0 + 32 * i + lane;
+      if (t >= a.max_tokens) break;
+      a.slots_dev[t] = pos[i] < 0 ? -1 : int64_t(page[i]) * P + row[i];
+      a.positions_dev[t] = pos[i];
+    }
   }
   for (int i = first; i < pages; i += step) {
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (page_end[mid] > i) hi = mid;
-      else lo = mid + 1;
-    }
+    const int lo = request_behind(page_end, 0, B - 1, i);
     const int have = pages_of(held_s[lo], div);
     a.block_tables_dev[(long long)lo * a.max_pages + have + i - (lo ? page_end[lo - 1] : 0)] =
         a.free_pages_dev[taken + i];
   }
 }
 
-}  // namespace
-
-cudaError_t launch_extend_tables(const cg_extend_args& a, cudaStream_t stream) {
+template <int kPer>
+cudaError_t launch(const cg_extend_args& a, int ctas, cudaStream_t stream) {
   const size_t smem = size_t(a.num_requests) * 12;
   if (smem > 48 * 1024 - 2048) {
     const cudaError_t err = cudaFuncSetAttribute(
-        extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRequests * 12);
+        extend_kernel<kPer>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRequests * 12);
     if (err != cudaSuccess) return err;
   }
-  // One CTA while a thread has at most four tokens to write; eight beyond, the
-  // largest portable cluster.
-  const int ctas = (a.max_tokens > 4 * kThreads || a.num_requests > kThreads) ? 8 : 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
@@ -232,8 +248,17 @@ cudaError_t launch_extend_tables(const cg_extend_args& a, cudaStream_t stream) {
   attr.val.clusterDim.x = ctas;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, extend_kernel, a, fast_div(uint32_t(a.page_tokens)));
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, extend_kernel<kPer>, a, fast_div(uint32_t(a.page_tokens)));
+}
+
+}  // namespace
+
+cudaError_t launch_extend_tables(const cg_extend_args& a, cudaStream_t stream) {
+  // One CTA while a thread has at most four tokens to write; eight beyond, the
+  // largest portable cluster.
+  return a.max_tokens > 4 * kThreads || a.num_requests > kThreads ? launch<4>(a, 8, stream)
+                                                                  : launch<1>(a, 1, stream);
 }
 
 }  // namespace cg
