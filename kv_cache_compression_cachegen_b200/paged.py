@@ -9,9 +9,9 @@ behind a shared prefix.  Each object holds what a program keeps between calls
 math runs in libcachegen's kernels.  Nothing here synchronises: data errors go
 to ``status``, which the caller reads after synchronising
 (``torch_api.status_of``).  Work is queued on ``stream``, or on the current
-stream of the object's device; an object is used by one stream at a time, and
-buffers that belong to another stream are the caller's to order, as everywhere
-in this package.
+stream of the object's device; an object is used by one stream at a time.  Its
+own buffers may be used on any stream; the caller's tensors are the caller's to
+order and to keep, as everywhere in this package.
 """
 from __future__ import annotations
 
@@ -57,6 +57,7 @@ class _Call:
         self.status = (torch.zeros(1, dtype=torch.int32, device=self.device)
                        if status is None else status)
         self._status = self._vector(self.status, "status", torch.int32, 1)
+        self._seen = {_raw_stream(self._index)}  # streams that self._buffers() are known to
 
     def _vector(self, t: torch.Tensor, name: str, dtype, count: int = 0) -> int:
         if t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous() or \
@@ -86,12 +87,28 @@ class _Call:
         raise ValueError("pool must be a contiguous [L, 2, num_pages, page_tokens, H, D] "
                          f"tensor of the object's type on {self.device}")
 
+    def _buffers(self) -> tuple:
+        """The object's own device buffers."""
+        return (self.status,)
+
+    def _meet(self, handle: int) -> None:
+        """Tell the caching allocator that a stream other than the one the
+        buffers were made on uses them, so that their memory is not handed out
+        again before that stream is done with them."""
+        s = (torch.cuda.ExternalStream(handle, device=self.device) if handle
+             else torch.cuda.default_stream(self.device))
+        for t in self._buffers():
+            t.record_stream(s)
+        self._seen.add(handle)
+
     def _launch(self, fn, stream, *args) -> None:
         """fn(*args, stream) with this object's device current."""
         if stream is None:
             handle = _raw_stream(self._index)
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if handle not in self._seen:
+            self._meet(handle)
         if _get_device() == self._index:
             rc = fn(*args, handle)
         else:
@@ -120,6 +137,9 @@ class PagedTables(_Call):
         self._args = ExtendArgs()
         self._ref = ctypes.byref(self._args)
         self._fn = library().cg_extend_tables
+
+    def _buffers(self) -> tuple:
+        return (self.status, self.kv_lens, self.q_starts, self.slots, self.positions, self.taken)
 
     def extend(self, held: torch.Tensor, added: torch.Tensor, block_tables: torch.Tensor,
                free_pages: torch.Tensor, taken: torch.Tensor | None = None,
@@ -222,7 +242,11 @@ class PagedAttention(_Call):
                                             self.max_requests, shared)
         if self.workspace is None or self.workspace.numel() < need:
             self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            self._seen = {_raw_stream(self._index)}
         self._has_shared = shared
+
+    def _buffers(self) -> tuple:
+        return self.status, self.workspace
 
     def reserve_shared(self) -> None:
         """Size the workspace for run_shared now (its first call does so

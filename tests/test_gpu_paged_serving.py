@@ -109,3 +109,25 @@ def test_two_streams_two_workspaces():
     for b, out in zip(batches, outs):
         want, _, tol = b.oracle()
         check_close(out, want, tol)
+
+
+def test_objects_outlived_by_their_work_on_another_stream():
+    # an object made on one stream, used on another and dropped at once: its
+    # workspace is not handed out again while that stream still works in it
+    from paged_util import Batch
+    H, Hq, D, P, T = 2, 8, 128, 16, torch.float16
+    b = Batch([3000, 700, 90], [1, 1, 1], Hq, H, D, P, T, seed=3, prefix=200)
+    q, pool, starts, lens, tables, ptable = b.device()
+    side = torch.cuda.Stream()
+    outs = [torch.empty_like(q) for _ in range(8)]
+    torch.cuda.synchronize()
+    for out in outs:
+        call = ta.PagedAttention((1, H, D), Hq, T, 3, 3, DEV)
+        call.run_shared(q, pool, 0, ptable, 200, starts, lens, tables, 1, out, stream=side)
+        size = call.workspace.numel()
+        del call
+        torch.empty(size, dtype=torch.uint8, device=DEV).fill_(255)
+    torch.cuda.synchronize()
+    want, _, tol = b.oracle()
+    for out in outs:
+        check_close(out, want, tol)
