@@ -482,7 +482,8 @@ typedef struct cg_attention_args {
   int64_t q_stride, out_stride;
   float* lse_dev;                  /* [num_tokens][Hq] log of the sum of exp(score), or NULL */
   const int32_t* q_starts_dev;     /* [B + 1] */
-  const int32_t* kv_lens_dev;      /* [B] tokens in the pool, the new ones included */
+  const int32_t* kv_lens_dev;      /* [B] tokens in the pool, the new ones included, at most
+                                      2^31 - 256 */
   const int32_t* block_tables_dev; /* [B][max_pages] */
   const uint16_t* pool_dev;
   int32_t* status_dev;

@@ -80,6 +80,8 @@ struct Request {
   int row0;           // position of its first new token among the keys (may be negative)
 };
 
+constexpr int kMostKeys = 0x7FFFFF00;  // a unit's last key is counted in 31 bits
+
 // False (and the request is left out) where the lengths do not fit the call.
 __device__ __forceinline__ bool load_request(const AttnParams& p, int r, Request& q) {
   const int a = p.q_starts[r], b = p.q_starts[r + 1], keys = p.kv_lens[r];
@@ -87,7 +89,7 @@ __device__ __forceinline__ bool load_request(const AttnParams& p, int r, Request
   q.tokens = 0;
   q.keys = 0;
   q.row0 = 0;
-  if (a < 0 || b < a || b > p.num_tokens || b - a > p.max_q || keys < 0 ||
+  if (a < 0 || b < a || b > p.num_tokens || b - a > p.max_q || keys < 0 || keys > kMostKeys ||
       int64_t(keys) > int64_t(p.max_pages) * p.page_tokens)
     return false;
   q.tokens = b - a;

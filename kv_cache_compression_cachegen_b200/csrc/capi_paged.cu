@@ -66,6 +66,7 @@ cg_status attention(const cg_shape* shape, const cg_attention_args* a, const int
   if (shared && (a->window != 0 || a->sinks != 0 || prefix_tokens < 0 ||
                  (prefix_tokens > 0 && missing4(prefix_table))))
     return CG_ERR_INVALID_ARG;
+  if (shared && prefix_tokens > 0x7FFFFF00) return CG_ERR_UNSUPPORTED;
   const uint64_t need =
       cg::attention_workspace(*shape, a->num_q_heads, a->num_tokens, a->num_requests, shared);
   if (a->workspace_bytes < need) return CG_ERR_CAPACITY;

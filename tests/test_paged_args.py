@@ -111,6 +111,7 @@ def test_attention_limits_and_workspace():
     assert _attention(shape=cg.Shape(4, 2, 272)) == cg.CG_ERR_UNSUPPORTED
     assert _attention(prefix=(None, 100)) == cg.CG_ERR_INVALID_ARG
     assert _attention(prefix=(256, -1)) == cg.CG_ERR_INVALID_ARG
+    assert _attention(prefix=(256, 2 ** 31 - 1)) == cg.CG_ERR_UNSUPPORTED
     # the shared form has no window
     assert _attention(prefix=(256, 100), window=8) == cg.CG_ERR_INVALID_ARG
     assert _attention(prefix=(256, 100), sinks=1) == cg.CG_ERR_INVALID_ARG
