@@ -340,6 +340,8 @@ struct Walk {
   // All threads of the block; cum_s has room for kScanSlots + 1.
   __device__ __forceinline__ bool begin(const AttnParams& p, const Lane& lane, int64_t* cum_s) {
     slots = total_slots<kTile>(p);
+    item0 = share0 = 0;
+    if (slots <= 32) return begin_warp(p, lane);
     const int64_t* line = lane.cum;
     if (!p.planned) {
       sum_line<kTile, kKeys>(p, cum_s);
@@ -348,14 +350,42 @@ struct Walk {
         for (int i = threadIdx.x; i <= slots; i += blockDim.x) lane.cum[i] = cum_s[i];
     }
     units = line[slots] * p.kv_heads;
+    if (!take_share(p, lane)) return false;
+    x = slot_of(line, slots, p.kv_heads, u);
+    cum = line[x];
+    return true;
+  }
+
+  // A short line: every warp sums it up by itself, a slot a lane, and nothing waits.
+  __device__ __forceinline__ bool begin_warp(const AttnParams& p, const Lane& lane) {
+    const int at = threadIdx.x & 31;
+    const int64_t own = at < slots ? slot_item<kTile, kKeys>(p, at, it) : 0;
+    int64_t sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(~0u, sum, o);
+      if (at >= o) sum += up;
+    }
+    const int64_t total = __shfl_sync(~0u, sum, 31);
+    if (blockIdx.x == 0 && threadIdx.x < 32) {
+      if (at < slots) lane.cum[at] = sum - own;
+      if (at == 0) lane.cum[slots] = total;
+    }
+    units = total * p.kv_heads;
+    const bool any = take_share(p, lane);
+    const uint32_t before =
+        __ballot_sync(~0u, any && at < slots && (sum - own) * p.kv_heads <= u);
+    x = any ? 31 - __clz(before) : 0;
+    cum = __shfl_sync(~0u, sum - own, x);
+    return any;
+  }
+
+  __device__ __forceinline__ bool take_share(const AttnParams& p, const Lane& lane) {
     ctas = shares_of<kTile>(p, lane, units);
-    item0 = share0 = 0;
     if (int(blockIdx.x) >= ctas) return false;
     u = share_of(blockIdx.x, units, ctas);
     u_end = share_of(blockIdx.x + 1, units, ctas);
     share0 = u;
-    x = slot_of(line, slots, p.kv_heads, u);
-    cum = line[x];
     return true;
   }
 

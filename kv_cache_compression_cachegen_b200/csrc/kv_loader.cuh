@@ -172,7 +172,7 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
   const int lane = threadIdx.x & 31;
   const int own = lane * box;  // the lane's keys: its box's first
   uint32_t stage = 0, phase = 1, unit_count = 0;
-  // One unit: where the lane's keys lie; looked up while the unit before is issued.
+  // One unit: where the lane's keys lie; looked up while the unit before comes.
   struct Ahead {
     int page, row_in_page, head;
     bool unit, seen;  // seen: some row of the item sees some of the keys
@@ -204,7 +204,6 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
   look_up();
   while (__all_sync(~0u, next.unit)) {
     const Ahead now = next;
-    look_up();
     const bool hole = now.seen && (now.page < 0 || now.page >= p.num_pages);
     const bool mine = now.seen && !hole;
     const int row = now.page * p.page_tokens + now.row_in_page;
@@ -232,6 +231,7 @@ __device__ __forceinline__ bool load_boxes(const AttnParams& p, Walk<kTile, kKey
           tma_load3_own(dst + b * kBlock + lane * box * 128, kv ? v_map : k_map, 64 * b, head, row,
                         ring.full + 8 * stage);
       }
+      if (kv == 0) look_up();  // the next unit, while this one's keys come
       if (++stage == kStages) stage = 0, phase ^= 1;
     }
     ++unit_count;
