@@ -177,8 +177,9 @@ __host__ __device__ constexpr int item_cost() {
 }
 
 // The item of slot x and its units for each kv head; 0 where it holds no rows.
+// from: a request whose slots start at or before x, or -1 to search for one.
 template <int kTile, int kKeys>
-__device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it) {
+__device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it, int from = -1) {
   const int own = own_slots<kTile>(p);
   if (x >= own) {
     it.request = -1;
@@ -189,7 +190,10 @@ __device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it) {
     it.row = (x - own) * kTile;
   } else {
     int lo = x;
-    if (kTile != kRowTile) {
+    if (kTile != kRowTile && from >= 0) {
+      lo = from;
+      while (lo + 1 < p.num_requests && slot_base<kTile>(p, lo + 1) <= x) ++lo;
+    } else if (kTile != kRowTile) {
       lo = 0;
       int hi = p.num_requests - 1;  // the last request whose slots start at or before x
       while (lo < hi) {
@@ -265,6 +269,10 @@ __device__ __forceinline__ int pool_row(const AttnParams& p, const int32_t* tabl
   return page * p.page_tokens + (key - col * p.page_tokens);
 }
 
+__device__ __forceinline__ void prefetch_line(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // CTA that holds unit u when `units` are dealt to `ctas`: share c is
 // [c * units / ctas, (c + 1) * units / ctas).
 __device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas) {
@@ -331,6 +339,7 @@ template <int kTile, int kKeys>
 struct Walk {
   int64_t u, u_end, share0, cum, units;
   int x, slots, ctas;
+  int known = -1;  // the slot that `it` and `cost` are of
   // the current part: units [first, last) of an item of `cost` units at `head`
   Item it;
   int64_t item0;  // its first unit
@@ -339,6 +348,11 @@ struct Walk {
 
   // All threads of the block; cum_s has room for kScanSlots + 1.
   __device__ __forceinline__ bool begin(const AttnParams& p, const Lane& lane, int64_t* cum_s) {
+    // the lengths are looked at in an order that waits: have their lines come first
+    for (int i = 32 * threadIdx.x; i <= p.num_requests; i += 32 * blockDim.x) {
+      prefetch_line(p.q_starts + i);
+      if (i < p.num_requests) prefetch_line(p.kv_lens + i);
+    }
     slots = total_slots<kTile>(p);
     item0 = share0 = 0;
     if (slots <= 32) return begin_warp(p, lane);
@@ -391,7 +405,11 @@ struct Walk {
 
   __device__ __forceinline__ bool next(const AttnParams& p) {
     while (u < u_end && x < slots) {
-      cost = slot_item<kTile, kKeys>(p, x, it);
+      if (known != x) {
+        // slots are taken in order: the request is the last one's or soon behind
+        cost = slot_item<kTile, kKeys>(p, x, it, known >= 0 ? it.request : -1);
+        known = x;
+      }
       if (cost == 0 || u >= (cum + cost) * p.kv_heads) {
         cum += cost;
         ++x;

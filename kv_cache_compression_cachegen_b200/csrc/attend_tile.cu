@@ -41,7 +41,13 @@ struct Geometry {
   static constexpr int kQBytes = 128 * 128;           // a 64-channel block of a query tile
   static constexpr int kBlock = kKeys * 128;          // a 64-channel block of a K or V tile
   static constexpr int kStage = DC * kBlock;
-  static constexpr int kSmem = kTiles * DC * kQBytes + kStages * kStage + 1024;
+  // Output rows pass through shared memory on their way out, 64 bytes of each of a
+  // warp's 32 rows at a time, so that four lanes write a row's and not one: a
+  // store that touches 32 rows holds the memory pipe for 32 cycles, and the last
+  // step of an item took 25,000 of them.  Rows 80 bytes apart: no bank conflicts.
+  static constexpr int kPitch = 80, kOutBytes = 32 * kPitch;
+  static constexpr int kOut = kTiles * DC * kQBytes + kStages * kStage;
+  static constexpr int kSmem = kOut + 4 * kTiles * kOutBytes + 1024;
   // Tensor memory columns of scores, weights and outputs (of tile 1: kStep on).
   // Products are only sure to follow one another in order where their shapes
   // are alike, so the next scores may overwrite weights that a product still
@@ -350,44 +356,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = div_of(row, p.group_div);
       const int64_t t = it.token0 + tok;
       const int qh = it.head * p.group + row - tok * p.group;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool direct = it.whole && !p.shared;
       const int64_t piece = int64_t(it.piece) * G::kRows + 128 * tile + r;
       const int64_t whole = (int64_t(prefix) * p.num_tokens + t) * p.q_heads + qh;
-      float* part = !it.whole ? p.tiles.pieces + piece * D : p.whole + whole * D;
-      const bool direct = it.whole && !p.shared;
-      uint16_t* out = p.out + t * p.out_stride + int64_t(qh) * D;
-      bool odd = !(l - l == 0.f);
-      for (int c = 0; c < D; c += 16) {
-        uint32_t o[16];
-        if (none) {
+      char* const mine =
+          !real    ? nullptr
+          : direct ? reinterpret_cast<char*>(p.out + t * p.out_stride + int64_t(qh) * D)
+          : it.whole ? reinterpret_cast<char*>(p.whole + whole * D)
+                     : reinterpret_cast<char*>(p.tiles.pieces + piece * D);
+      // this lane stores 16 bytes of rows 8 i + lane / 4
+      char* rows[4];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = 0;
-        } else {
-          tmem_load16(t_o + c, o);
-        }
+      for (int i = 0; i < 4; ++i)
+        rows[i] = reinterpret_cast<char*>(
+                      __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine), 8 * i + (lane >> 2)));
+      const uint32_t pass = base + G::kOut + warp * G::kOutBytes;
+      const uint32_t give = pass + lane * G::kPitch, take = pass + (lane >> 2) * G::kPitch + 16 * (lane & 3);
+      // 64 bytes of each row through shared memory, `bytes` of them the row's
+      const auto put = [&](const uint32_t (&words)[16], int offset, int bytes) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float v = __uint_as_float(o[j]);
-          odd |= !(v - v == 0.f);
-        }
-        if (real && direct) {
+        for (int k = 0; k < 4; ++k) st_shared16(give + 16 * k, words + 4 * k);
+        __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 16; j += 8) {
-            uint32_t x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = T::pack(__uint_as_float(o[j + 2 * e]) * inv,
-                             __uint_as_float(o[j + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(out + c + j) = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        } else if (real) {
-#pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<uint4*>(part + c + j) =
-                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = ld_shared16(take + 8 * i * G::kPitch);
+          if (rows[i] != nullptr && 16 * (lane & 3) < bytes)
+            *reinterpret_cast<uint4*>(rows[i] + offset + 16 * (lane & 3)) = v;
         }
         __syncwarp();
+      };
+      float2 odd2 = make_float2(l - l, 0.f);  // NaN once a sum is not finite
+      const float2 zero2 = make_float2(0.f, 0.f);
+      uint32_t words[16];
+      if (direct) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float2 inv2 = make_float2(inv, inv);
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (none) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+          } else {
+            tmem_load32(t_o + c, o);  // past the channels, where those are no multiple of 32
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 v = make_float2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+            if (j < 8 || c + 16 < D) odd2 = fma_pair(v, zero2, odd2);
+            const float2 y = fma_pair(v, inv2, zero2);
+            words[j] = T::pack(y.x, y.y);
+          }
+          put(words, 2 * c, 2 * (D - c));
+        }
+      } else {
+        for (int c = 0; c < D; c += 16) {
+          if (none) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) words[j] = 0;
+          } else {
+            tmem_load16(t_o + c, words);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            odd2 = fma_pair(make_float2(__uint_as_float(words[j]), __uint_as_float(words[j + 1])),
+                            zero2, odd2);
+          put(words, 4 * c, 64);
+        }
       }
+      const bool odd = !(odd2.x + odd2.y == 0.f);
       if (real) {
         if (!direct) (it.whole ? p.whole_stats[whole] : p.tiles.stats[piece]) = make_float2(m, l);
         else if (p.lse != nullptr) p.lse[t * p.q_heads + qh] = log_sum(m, l);
@@ -433,47 +469,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kQueryWarp) {
       // ---- queries
       uint32_t q_phase = 3;  // a bit for each query tile
-      bool ok = any, noted = false;
+      bool ok = any;
       if (!any && lane == 0) w.note_cut(p.tiles, false);
-      for (uint32_t n = 0; ok; ++n) {
-        const bool more = w.next(p);
-        const Item& it = w.it;
-        if (!noted && lane == 0) w.note_cut(p.tiles, more);
-        noted = true;
-        if (!(ok = mbar_wait(bar.item_free + 8 * (n % kItems), ((n / kItems) & 1) ^ 1, dead))) break;
+      const auto deal = [&](uint32_t n, bool more) {
+        if (!mbar_wait(bar.item_free + 8 * (n % kItems), ((n / kItems) & 1) ^ 1, dead)) return false;
         if (lane == 0) {
+          const Item& it = w.it;
           deals[n % kItems] = Deal{w.first, max(w.first, w.last), it.span.sink_units,
                                    it.span.first_unit, more ? it.rows : 0, it.row, it.req.first,
                                    it.req.row0, it.request, w.head, w.piece, w.whole};
           mbar_arrive(bar.item_full + 8 * (n % kItems));
         }
         __syncwarp();
-        if (!more) break;
-        if (w.first >= w.last) continue;
-        for (int tile = 0; tile < (it.rows > 128 ? 2 : 1); ++tile) {
+        return true;
+      };
+      bool more = ok && w.next(p);
+      if (ok && lane == 0) w.note_cut(p.tiles, more);
+      ok = ok && deal(0, more);
+      // an item is dealt before the queries of the one before it are waited for
+      for (uint32_t n = 1; ok && more; ++n) {
+        const int rows = w.it.rows, row = w.it.row, token0 = w.it.req.first;
+        const int first_head = w.head * p.group;
+        const bool none = w.first >= w.last;
+        more = w.next(p);
+        if (!(ok = deal(n, more))) break;
+        if (none) continue;
+        for (int tile = 0; tile < (rows > 128 ? 2 : 1); ++tile) {
           if (!(ok = mbar_wait(bar.q_free + 8 * tile, (q_phase >> tile) & 1, dead))) break;
           q_phase ^= 1u << tile;
           const uint32_t dst = q_smem + tile * DC * G::kQBytes;
-          const int row0 = it.row + 128 * tile;
+          const int row0 = row + 128 * tile;
           if (by_map) {
             // rows behind the item's are other tokens' or zeros, and are not used
             mbar_expect(bar.q_full + 8 * tile, DC * G::kQBytes);
-            const int head = __shfl_sync(~0u, w.head * p.group, 0);
-            const int token = __shfl_sync(~0u, it.req.first + div_of(row0, p.group_div), 0);
+            const int head = __shfl_sync(~0u, first_head, 0);
+            const int token = __shfl_sync(~0u, token0 + div_of(row0, p.group_div), 0);
             for (int b = 0; b < DC; ++b)
               tma_load3(dst + b * G::kQBytes, &q_map, 64 * b, head, token, bar.q_full + 8 * tile);
             continue;
           }
 #pragma unroll 4
           for (int i = 0; i < 128; i += 4) {  // eight lanes a row
-            const int r = i + (lane >> 3), c = lane & 7, row = row0 + r;
-            const int tok = div_of(row, p.group_div);
-            const uint16_t* src = p.q + int64_t(it.req.first + tok) * p.q_stride +
-                                  int64_t(w.head * p.group + row - tok * p.group) * D + 8 * c;
+            const int r = i + (lane >> 3), c = lane & 7, at = row0 + r;
+            const int tok = div_of(at, p.group_div);
+            const uint16_t* src = p.q + int64_t(token0 + tok) * p.q_stride +
+                                  int64_t(first_head + at - tok * p.group) * D + 8 * c;
 #pragma unroll
             for (int b = 0; b < DC; ++b) {
               uint4 v = make_uint4(0, 0, 0, 0);
-              if (128 * tile + r < it.rows && 64 * b + 8 * c < D)
+              if (128 * tile + r < rows && 64 * b + 8 * c < D)
                 v = *reinterpret_cast<const uint4*>(src + 64 * b);
               v.x ^= p.q_flip, v.y ^= p.q_flip, v.z ^= p.q_flip, v.w ^= p.q_flip;
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
