@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 384;  // 168 registers a thread: a softmax thread holds 128 scores
 constexpr int kMmaWarp = 8, kQueryWarp = 9, kLoadWarp = 10;
+constexpr int kUnroll = 2;  // of the loops over 32 scores; one and four were slower
 constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
 
 template <int DC>
@@ -33,11 +34,11 @@ struct Geometry {
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kKeys = DC <= 2 ? 128 : 64;    // keys of a unit
   static constexpr int kStages = 4;                   // K and V tiles in flight
-  // Pairs j of weights with (j & kPolynomial) == 8 go to exp2_pair.  With up to 64
+  // Pairs j of 16 with (j & kPolynomial) == 4 go to exp2_pair.  With up to 64
   // channels the exponentials bound the kernel, and an eighth of them there made
   // two prompts of 8,192 tokens 835 us (none: 889, a quarter: 859); with 128 a
   // sixteenth 1,042 (none: 1,105, a quarter: 1,154).
-  static constexpr int kPolynomial = DC == 1 ? 15 : 31;
+  static constexpr int kPolynomial = DC == 1 ? 7 : 15;
   static constexpr int kQBytes = 128 * 128;           // a 64-channel block of a query tile
   static constexpr int kBlock = kKeys * 128;          // a 64-channel block of a K or V tile
   static constexpr int kStage = DC * kBlock;
@@ -269,30 +270,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_wait(bar.s_full + 8 * tile, s_phase, dead))) break;
         s_phase ^= 1;
         tc_fence_after();
-        const uint4 hole = *reinterpret_cast<const uint4*>(no_page[unit_count % kNoted]);
-        uint32_t raw[G::kKeys];
-        tmem_load<G::kKeys>(t_s, raw);
-        if (!full || (hole.x | hole.y | hole.z | hole.w) != 0) {
-          mixed = true;
-          // keys before `past` are behind the window
-          const int past = window == 0 ? 0 : int(max(0ll, (long long)pos - window + 1));
-          const uint32_t hole4[4] = {hole.x, hole.y, hole.z, hole.w};
+        const uint32_t* hole = no_page[unit_count % kNoted];
+        uint32_t holes = 0;
 #pragma unroll
-          for (int i = 0; i < G::kKeys / 32; ++i) {
+        for (int i = 0; i < G::kKeys / 32; ++i) holes |= hole[i];
+        const bool hide = !full || holes != 0;
+        mixed |= hide;
+        // keys before `past` are behind the window
+        const int past = window == 0 ? 0 : int(max(0ll, (long long)pos - window + 1));
+        // 32 scores at a time, twice: first the maximum, then the weights.  Short
+        // loops, and the scores read again, rather than a row's 128 in registers
+        // and all of it unrolled: a kernel's first pass over its instructions costs
+        // more than its arithmetic, and a call of a few items is little else.
+        uint32_t raw[32];
+        const auto scores = [&](int i) {
+          tmem_load32(t_s + 32 * i, raw);
+          if (hide) {
             const int from = key0 + 32 * i;
             const uint32_t seen =
-                below(pos + 1 - from) & (~below(past - from) | below(sinks - from)) & ~hole4[i];
+                below(pos + 1 - from) & (~below(past - from) | below(sinks - from)) & ~hole[i];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!((seen >> j) & 1)) raw[32 * i + j] = __float_as_uint(kNegInf);
+              if (!((seen >> j) & 1)) raw[j] = __float_as_uint(kNegInf);
           }
-        }
-        // NaN if any score is
-        float top[2] = {kNegInf, kNegInf};
+        };
+        float top[2] = {kNegInf, kNegInf};  // NaN if any score is
+#pragma unroll kUnroll
+        for (int i = 0; i < G::kKeys / 32; ++i) {
+          scores(i);
 #pragma unroll
-        for (int j = 0; j < G::kKeys; j += 4) {
-          top[0] = max3_nan(top[0], __uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
-          top[1] = max3_nan(top[1], __uint_as_float(raw[j + 2]), __uint_as_float(raw[j + 3]));
+          for (int j = 0; j < 32; j += 4) {
+            top[0] = max3_nan(top[0], __uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
+            top[1] = max3_nan(top[1], __uint_as_float(raw[j + 2]), __uint_as_float(raw[j + 3]));
+          }
         }
         const float most = max3_nan(top[0], top[1], kNegInf) * p.scale_log2;
         const bool move = !(most <= m + kSlack);
@@ -319,28 +329,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 shift2 = make_float2(shift, shift);
         // By halves of the unit, so that the product with the first half's values
         // runs while the second half is computed.
+#pragma unroll kUnroll
+        for (int i = 0; i < G::kKeys / 32; ++i) {
+          scores(i);
+          uint32_t weights[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int j = h * (G::kKeys / 2); j < (h + 1) * (G::kKeys / 2); j += 2) {
-            const float2 x = fma_pair(
-                make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])), scale2, shift2);
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = fma_pair(make_float2(__uint_as_float(raw[2 * j]),
+                                                  __uint_as_float(raw[2 * j + 1])),
+                                      scale2, shift2);
             // a few on the multiply-add pipe: see exp2_pair
-            const float2 e = (j & G::kPolynomial) == 8
+            const float2 e = (j & G::kPolynomial) == 4
                                  ? exp2_pair(x)
                                  : make_float2(exp2_fast(x.x), exp2_fast(x.y));
-            sum[(j >> 1) & 1] = add_pair(sum[(j >> 1) & 1], e);
+            sum[j & 1] = add_pair(sum[j & 1], e);
             // rounded to the pool's type for the product with V: half a step of it
             // relative to each weight; the sum is not
-            raw[j / 2] = T::pack(e.x, e.y);
+            weights[j] = T::pack(e.x, e.y);
           }
-          constexpr int kColumns = G::kKeys / 4;
-          if constexpr (kColumns == 32) tmem_store32(t_p + h * kColumns, raw + h * kColumns);
-          else tmem_store16(t_p + h * kColumns, raw + h * kColumns);
-          tmem_store_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar.p_full + 8 * (2 * tile + h));
+          // (where the weights take their scores' place, it is one already read)
+          tmem_store16(t_p + 16 * i, weights);
+          constexpr int kPerHalf = G::kKeys / 64;
+          if ((i + 1) % kPerHalf == 0) {
+            tmem_store_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.p_full + 8 * (2 * tile + i / kPerHalf));
+          }
         }
         // nothing seen so far: exp2_pair leaves 2^-125 where the weight is zero
         l = m == kNegInf ? 0.f : l + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
