@@ -228,20 +228,6 @@ __device__ __forceinline__ int row_position(const AttnParams& p, const Item& it,
   return it.request < 0 ? it.req.row0 : it.req.row0 + div_of(row, p.group_div);
 }
 
-// The last request that starts at or before packed row t; all lanes of a warp.
-__device__ __forceinline__ int request_of(const AttnParams& p, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = p.num_requests;
-  while (n > 1) {
-    const int step = (n + 31) / 32, at = lo + lane * step;
-    const bool before = lane * step < n && (lane == 0 || p.q_starts[at] <= t);
-    const int k = __popc(__ballot_sync(~0u, before)) - 1;  // starts do not fall
-    lo += k * step;
-    n = min(step, n - k * step);
-  }
-  return lo;
-}
-
 // CTAs that get a share: no share is empty.  In step: where a prefix is larger
 // than the L2 cache, its row tiles should read the same keys at the same time,
 // and do if each has the same number of shares (the line goes tile by tile, and

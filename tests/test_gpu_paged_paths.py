@@ -234,3 +234,17 @@ def test_keys_not_finite():
             good[added + first:] = False
             check_close(out[good.to(DEV)], want[good], tol[good])
             assert torch.isnan(out[~good.to(DEV)]).all()
+
+
+def test_first_call_captured():
+    # nothing has to run before a capture: kernels that no call has used yet
+    b = build([41, 50], [1, 3], 4, 2, 48, 16, torch.bfloat16, 0, 9)
+    call = ta.PagedAttention((1, 2, 48), 4, torch.bfloat16, 4, 2, DEV)
+    out = torch.empty_like(b["q"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.run(b["q"], b["pool"], 0, b["starts"], b["lens"], b["tables"], 3, out)
+    graph.replay()
+    torch.cuda.synchronize()
+    check_close(out, *reference(b))

@@ -131,3 +131,26 @@ def test_objects_outlived_by_their_work_on_another_stream():
     want, _, tol = b.oracle()
     for out in outs:
         check_close(out, want, tol)
+
+
+def test_a_step_that_fails_leaves_the_calls_behind_it_without_rows():
+    # too few free pages: no table, no pool row and no output row is written
+    H, Hq, D, P, T, B = 2, 4, 64, 16, torch.float16, 3
+    tables = ta.PagedTables(B, 8, P, 10, DEV)
+    append = ta.PagedAppend((1, H, D), Hq, T, DEV)
+    attend = ta.PagedAttention((1, H, D), Hq, T, 8, B, DEV)
+    pool = torch.full((1, 2, 10, P, H, D), 5.0, dtype=T, device=DEV)
+    bt = torch.full((B, 4), -1, dtype=torch.int32, device=DEV)
+    free = torch.arange(2, dtype=torch.int32, device=DEV)
+    added = torch.ones(B, dtype=torch.int32, device=DEV)
+    qkv = torch.randn(8, Hq + 2 * H, D, device=DEV).to(T)
+    q, out = (torch.full((8, Hq, D), 3.0, dtype=T, device=DEV) for _ in range(2))
+    tables.extend(tables.kv_lens, added, bt, free)
+    append.append(qkv[:, :Hq], qkv[:, Hq:Hq + H], qkv[:, Hq + H:], q, pool, 0, tables.positions,
+                  tables.slots, ta.rope_table(8, D, DEV))
+    attend.run(q, pool, 0, tables.q_starts, tables.kv_lens, bt, 1, out)
+    attend.run_shared(q, pool, 0, free, 20, tables.q_starts, tables.kv_lens, bt, 1, out)
+    torch.cuda.synchronize()
+    assert ta.status_of(tables.status) == 2  # CG_ERR_CAPACITY
+    assert ta.status_of(append.status) == 0 and ta.status_of(attend.status) == 0
+    assert (pool == 5).all() and (q == 3).all() and (out == 3).all() and (bt == -1).all()
