@@ -23,9 +23,8 @@
 namespace cg {
 namespace {
 
-constexpr int kThreads = 384;  // 168 registers a thread: a softmax thread holds 128 scores
+constexpr int kThreads = 384;  // up to 168 registers a thread; a softmax thread takes 150
 constexpr int kMmaWarp = 8, kQueryWarp = 9, kLoadWarp = 10;
-constexpr int kUnroll = 2;  // of the loops over 32 scores; one and four were slower
 constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
 
 template <int DC>
@@ -34,18 +33,19 @@ struct Geometry {
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kKeys = DC <= 2 ? 128 : 64;    // keys of a unit
   static constexpr int kStages = 4;                   // K and V tiles in flight
-  // Pairs j of 16 with (j & kPolynomial) == 4 go to exp2_pair.  With up to 64
-  // channels the exponentials bound the kernel, and an eighth of them there made
-  // two prompts of 8,192 tokens 835 us (none: 889, a quarter: 859); with 128 a
-  // sixteenth 1,042 (none: 1,105, a quarter: 1,154).
+  // Pairs j of 16 with (j & kPolynomial) == 4 go to exp2_pair: an eighth of a row
+  // with up to 64 channels, a sixteenth beyond.  Two prompts of 8,192 tokens, 64
+  // channels: 943 us, without any 977.  128 channels: 1,075, without 1,114, an
+  // eighth or a quarter 1,060 to 1,086 (and 1,066 for the sixteenth beside them).
   static constexpr int kPolynomial = DC == 1 ? 7 : 15;
   static constexpr int kQBytes = 128 * 128;           // a 64-channel block of a query tile
   static constexpr int kBlock = kKeys * 128;          // a 64-channel block of a K or V tile
   static constexpr int kStage = DC * kBlock;
   // Output rows pass through shared memory on their way out, 64 bytes of each of a
-  // warp's 32 rows at a time, so that four lanes write a row's and not one: a
-  // store that touches 32 rows holds the memory pipe for 32 cycles, and the last
-  // step of an item took 25,000 of them.  Rows 80 bytes apart: no bank conflicts.
+  // warp's 32 rows at a time, so that four lanes write 64 bytes of a row and not
+  // each lane 16 of its own: 148 requests of 64 tokens behind 64, an item an SM,
+  // took 75.0 us instead of 85.3, one item 22.8 instead of 24.1.  Rows 80 bytes
+  // apart: no bank conflicts.
   static constexpr int kPitch = 80, kOutBytes = 32 * kPitch;
   static constexpr int kOut = kTiles * DC * kQBytes + kStages * kStage;
   static constexpr int kSmem = kOut + 4 * kTiles * kOutBytes + 1024;
@@ -278,28 +278,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         mixed |= hide;
         // keys before `past` are behind the window
         const int past = window == 0 ? 0 : int(max(0ll, (long long)pos - window + 1));
-        // 32 scores at a time, twice: first the maximum, then the weights.  Short
-        // loops, and the scores read again, rather than a row's 128 in registers
-        // and all of it unrolled: a kernel's first pass over its instructions costs
-        // more than its arithmetic, and a call of a few items is little else.
-        uint32_t raw[32];
+        // 64 scores at a time, twice: first the maximum, then the weights.  Loops, and
+        // the scores read again, rather than a row's 128 in registers and all of it
+        // unrolled: the first pass over more instructions costs a short item more
+        // than the second load.  148 requests of 64 tokens behind 64: 75.5 us against
+        // 87.9; two prompts of 8,192 tokens: 1,015 against 1,036, with 64 channels 890
+        // against 871.  32 at a time wait for twice as many loads: 75.3, 1,060, 915.
+        uint32_t raw[64];
         const auto scores = [&](int i) {
-          tmem_load32(t_s + 32 * i, raw);
+          tmem_load64(t_s + 64 * i, raw);
           if (hide) {
-            const int from = key0 + 32 * i;
-            const uint32_t seen =
-                below(pos + 1 - from) & (~below(past - from) | below(sinks - from)) & ~hole[i];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((seen >> j) & 1)) raw[j] = __float_as_uint(kNegInf);
+            for (int w = 0; w < 2; ++w) {
+              const int from = key0 + 64 * i + 32 * w;
+              const uint32_t seen = below(pos + 1 - from) &
+                                    (~below(past - from) | below(sinks - from)) & ~hole[2 * i + w];
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((seen >> j) & 1)) raw[32 * w + j] = __float_as_uint(kNegInf);
+            }
           }
         };
         float top[2] = {kNegInf, kNegInf};  // NaN if any score is
-#pragma unroll kUnroll
-        for (int i = 0; i < G::kKeys / 32; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < G::kKeys / 64; ++i) {
           scores(i);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < 64; j += 4) {
             top[0] = max3_nan(top[0], __uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
             top[1] = max3_nan(top[1], __uint_as_float(raw[j + 2]), __uint_as_float(raw[j + 3]));
           }
@@ -329,33 +334,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 shift2 = make_float2(shift, shift);
         // By halves of the unit, so that the product with the first half's values
         // runs while the second half is computed.
-#pragma unroll kUnroll
-        for (int i = 0; i < G::kKeys / 32; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < G::kKeys / 64; ++i) {
           scores(i);
-          uint32_t weights[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 x = fma_pair(make_float2(__uint_as_float(raw[2 * j]),
-                                                  __uint_as_float(raw[2 * j + 1])),
-                                      scale2, shift2);
-            // a few on the multiply-add pipe: see exp2_pair
-            const float2 e = (j & G::kPolynomial) == 4
-                                 ? exp2_pair(x)
-                                 : make_float2(exp2_fast(x.x), exp2_fast(x.y));
-            sum[j & 1] = add_pair(sum[j & 1], e);
-            // rounded to the pool's type for the product with V: half a step of it
-            // relative to each weight; the sum is not
-            weights[j] = T::pack(e.x, e.y);
+          for (int w = 0; w < 2; ++w) {
+            uint32_t weights[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 x = fma_pair(make_float2(__uint_as_float(raw[32 * w + 2 * j]),
+                                                    __uint_as_float(raw[32 * w + 2 * j + 1])),
+                                        scale2, shift2);
+              // a few on the multiply-add pipe: see exp2_pair
+              const float2 e = (j & G::kPolynomial) == 4
+                                   ? exp2_pair(x)
+                                   : make_float2(exp2_fast(x.x), exp2_fast(x.y));
+              sum[j & 1] = add_pair(sum[j & 1], e);
+              // rounded to the pool's type for the product with V: half a step of it
+              // relative to each weight; the sum is not
+              weights[j] = T::pack(e.x, e.y);
+            }
+            // (where the weights take their scores' place, it is one already read)
+            tmem_store16(t_p + 32 * i + 16 * w, weights);
           }
-          // (where the weights take their scores' place, it is one already read)
-          tmem_store16(t_p + 16 * i, weights);
-          constexpr int kPerHalf = G::kKeys / 64;
-          if ((i + 1) % kPerHalf == 0) {
-            tmem_store_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar.p_full + 8 * (2 * tile + i / kPerHalf));
-          }
+          constexpr int kHalves = 128 / G::kKeys;  // of the unit in 64 scores
+          tmem_store_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0)
+            for (int h = i * kHalves; h < (i + 1) * kHalves; ++h)
+              mbar_arrive(bar.p_full + 8 * (2 * tile + h));
         }
         // nothing seen so far: exp2_pair leaves 2^-125 where the weight is zero
         l = m == kNegInf ? 0.f : l + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
