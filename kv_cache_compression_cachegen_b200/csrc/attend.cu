@@ -224,7 +224,7 @@ Workspace workspace_of(const cg_shape& s, int Hq, int tokens, int requests, bool
 
 template <typename T, int kTile, int kKeys>
 cudaError_t launch_all(AttnParams& p, int sms, cudaStream_t stream) {
-  p.rows.ctas = std::min(kMaxRowCtas, sms * kRowCtasPerSm);
+  p.rows.ctas = std::min(kMaxRowCtas, sms * row_ctas_per_sm(p.dim, most_rows(p)));
   p.rows.tile = kRowTile;
   const bool tiles = p.tiled || (p.shared && !p.prefix_small);
   p.tiles.ctas = tiles ? std::min(kMaxCtas, sms) : 0;

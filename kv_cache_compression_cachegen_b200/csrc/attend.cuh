@@ -154,6 +154,17 @@ __device__ __forceinline__ int total_slots(const AttnParams& p) {
          (prefix ? int((int64_t(p.num_tokens) * p.group + kTile - 1) / kTile) : 0);
 }
 
+// The most rows that an item of the rows kernel can have: a request's, or the
+// whole batch's under a prefix.
+inline int64_t most_rows(const AttnParams& p) {
+  const int64_t tokens =
+      p.shared && p.prefix_small ? p.num_tokens : (p.max_q < p.num_tokens ? p.max_q : p.num_tokens);
+  return tokens * p.group;
+}
+constexpr int row_ctas_per_sm(int dim, int64_t rows) {
+  return dim > 128 && rows > 8 ? 1 : kRowCtasPerSm;
+}
+
 // Query rows of a kv head in the whole batch.
 __device__ __forceinline__ int batch_rows(const AttnParams& p) {
   int n = p.q_starts[p.num_requests];

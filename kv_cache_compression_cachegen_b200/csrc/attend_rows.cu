@@ -31,9 +31,14 @@ constexpr float kSlack = 8.f;  // log2 of how far a weight may pass one
 static_assert(kRowKeys == 16 * kWarps, "each warp takes 16 keys of a unit");
 static_assert(kJoinBytes >= (kScanSlots + 1) * 8, "the line's sums lie there at first");
 
-template <int DC>
+template <int DC, int NR>
 struct Shape {
-  static constexpr int kStages = DC == 4 ? 3 : (DC == 2 ? 6 : 12);
+  // Two CTAs an SM, but one where sixteen rows have more than 128 channels: 168
+  // registers a thread hold neither those rows' sums nor their queries.  14 requests
+  // of 113 keys, 32 kv heads of 256 under 16 rows each: 70 us against 91 with two;
+  // of 5,001 keys 823 against 1,083.
+  static constexpr int kCtasPerSm = row_ctas_per_sm(64 * DC, 8 * NR);
+  static constexpr int kStages = (DC == 4 ? 3 : (DC == 2 ? 6 : 12)) * kRowCtasPerSm / kCtasPerSm;
   static constexpr int kStage = DC * kRowKeys * 128;
   // a row of a warp's output for the join: four channels more, so that the four
   // rows that a store touches fall on different banks
@@ -67,9 +72,9 @@ __device__ __forceinline__ void compute_sync() {
 
 // NR: products of eight query rows, 1 or 2.
 template <typename T, int DC, int NR>
-__global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
+__global__ void __launch_bounds__(kThreads, Shape<DC, NR>::kCtasPerSm)
     rows_kernel(AttnParams p, const __grid_constant__ KvMaps maps) {
-  using S = Shape<DC>;
+  using S = Shape<DC, NR>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[2 * S::kStages];
   __shared__ uint32_t no_page[kNoted][4];
@@ -425,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
 
 template <typename T, int DC, int NR>
 cudaError_t launch(const AttnParams& p, bool early, cudaStream_t stream) {
-  using S = Shape<DC>;
+  using S = Shape<DC, NR>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t err = allow_smem(rows_kernel<T, DC, NR>, S::kSmem, done);
   if (err != cudaSuccess) return err;
@@ -435,9 +440,7 @@ cudaError_t launch(const AttnParams& p, bool early, cudaStream_t stream) {
 
 template <typename T, int DC>
 cudaError_t launch_dim(const AttnParams& p, bool early, cudaStream_t stream) {
-  // can an item have more than eight rows?
-  const int64_t most = int64_t(p.prefix_small ? p.num_tokens : p.max_q) * p.group;
-  return most > 8 ? launch<T, DC, 2>(p, early, stream) : launch<T, DC, 1>(p, early, stream);
+  return most_rows(p) > 8 ? launch<T, DC, 2>(p, early, stream) : launch<T, DC, 1>(p, early, stream);
 }
 
 template <typename T>

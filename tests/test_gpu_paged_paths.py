@@ -248,3 +248,19 @@ def test_first_call_captured():
     graph.replay()
     torch.cuda.synchronize()
     check_close(out, *reference(b))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [128, 160, 256])
+def test_nine_to_sixteen_rows_of_many_channels(dim, dtype):
+    # items of 8, 16 and 9 rows a kv head, some cut; then of 16 rows under more tokens
+    b = build([700, 130, 1, 2050], [1, 2, 1, 2], 16, 2, dim, 16, dtype, 0, 9)
+    call = ta.PagedAttention((1, 2, dim), 16, dtype, 6, 4, DEV)
+    out = torch.empty_like(b["q"])
+    call.run(b["q"], b["pool"], 0, b["starts"], b["lens"], b["tables"], 2, out)
+    check_close(out, *reference(b))
+    b = build([700, 130, 90], [3, 1, 2], 15, 3, dim, 16, dtype, 0, 9)
+    call = ta.PagedAttention((1, 3, dim), 15, dtype, 6, 3, DEV)
+    out = torch.empty_like(b["q"])
+    call.run(b["q"], b["pool"], 0, b["starts"], b["lens"], b["tables"], 3, out, window=100)
+    check_close(out, *reference(b, window=100))
