@@ -30,7 +30,7 @@ CODEC_SOURCES = ["csrc/capi.cu", "csrc/encode.cu", "csrc/decode.cu", "csrc/stati
                  "csrc/attend.cu", "csrc/attend_rows.cu", "csrc/attend_tile.cu",
                  "csrc/attend_maps.cu"]
 CODEC_HEADERS = ["csrc/cg_common.cuh", "csrc/paged.cuh", "csrc/attend.cuh",
-                 "csrc/tcgen05.cuh", "csrc/kv_loader.cuh"]
+                 "csrc/tcgen05.cuh", "csrc/kv_loader.cuh", "csrc/shares.cuh"]
 SYNTH_SOURCES = ["synth/kvsynth.cu"]
 
 LIB_CODEC = PKG / "libcachegen.so"

@@ -8,8 +8,6 @@
 namespace cg {
 namespace {
 
-constexpr int kMaxCtas = 160;  // of the tile kernel, one an SM
-constexpr int kMaxRowCtas = kMaxCtas * kRowCtasPerSm;
 constexpr int64_t kInStepBytes = 64 << 20;  // half of the L2 cache
 
 // Block 0 sums up the rows kernel's line, block 1 the tile kernel's.

@@ -25,12 +25,12 @@
 #include <cuda.h>  // tensor-map types only; the encoder is looked up at run time
 
 #include "paged.cuh"
+#include "shares.cuh"
 
 namespace cg {
 
 constexpr int kRowTile = 16;   // query rows of an item of the rows kernel (one matrix tile)
 constexpr int kRowKeys = 64;   // keys of a unit there
-constexpr int kRowCtasPerSm = 2;
 constexpr int kScanSlots = 1024;  // slots of a line that every CTA sums up by itself
 
 // The line of work of one of the two kernels, in the workspace.
@@ -271,20 +271,6 @@ __device__ __forceinline__ int pool_row(const AttnParams& p, const int32_t* tabl
 
 __device__ __forceinline__ void prefetch_line(const void* p) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
-}
-
-// CTA that holds unit u when `units` are dealt to `ctas`: share c is
-// [c * units / ctas, (c + 1) * units / ctas).
-__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas) {
-  if (units < (1 << 24))  // 32 bits do, for fewer than 256 CTAs
-    return int((uint32_t(u + 1) * uint32_t(ctas) - 1) / uint32_t(units));
-  return int(((u + 1) * ctas - 1) / units);
-}
-
-// First unit of share c.
-__device__ __forceinline__ int64_t share_of(int c, int64_t units, int ctas) {
-  if (units < (1 << 24)) return uint32_t(units) * uint32_t(c) / uint32_t(ctas);
-  return units * c / ctas;
 }
 
 // Units of one head before each slot of a line, and of the whole line behind
