@@ -84,11 +84,14 @@ struct Deal {
 // 1.5 * 2^23, a polynomial for 2^(x - n) on [-1/2, 1/2], n added to the exponent.
 // The coefficients are the minimax ones of degree 5 for the relative error (Remez
 // exchange), 2^-23.7, and 2^-22 as evaluated in fp32 -- what ex2.approx has.
-// Below -125 the result stays 2^-125.
+// Below -126 the result runs out of exponent, as ex2.approx.ftz's does: at -127 and
+// under it is one unit in the last place above zero, 2^-149, which rounds to a weight
+// of zero in both types, so that the value of a hidden key (score -infinity) cannot
+// show, however large.  (r is not negative at -127, so the exponent does not wrap.)
 __device__ __forceinline__ float2 exp2_pair(float2 x) {
   const float2 magic = make_float2(12582912.f, 12582912.f);
   const float2 minus = make_float2(-12582912.f, -12582912.f);
-  x = make_float2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
   const float2 t = add_pair(x, magic);
   const float2 n = add_pair(t, minus);
   const float2 r = fma_pair(n, make_float2(-1.f, -1.f), x);
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = i * kHalves; h < (i + 1) * kHalves; ++h)
               mbar_arrive(bar.p_full + 8 * (2 * tile + h));
         }
-        // nothing seen so far: exp2_pair leaves 2^-125 where the weight is zero
+        // nothing seen so far: exp2_pair leaves 2^-149 where the weight is zero
         l = m == kNegInf ? 0.f : l + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
       }
       if (!ok) break;
