@@ -203,8 +203,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
         __syncwarp(group_mask);  // q_out may be q: all partners are read before any value is stored
       }
       if (turn) {
+        // A lane may hold the last turned channels and the first that are not: those
+        // keep their value whatever lies beside it.  (With halves rot is a multiple
+        // of 16, and a lane has the one or the other.)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(z[i], si[i], y[i] * co[i]);
+        for (int i = 0; i < 8; ++i)
+          if (TURN == kHalves || e0 + i < p.rot) y[i] = fmaf(z[i], si[i], y[i] * co[i]);
       }
     }
     raw[u] = make_uint4(T::pack(y[0], y[1]), T::pack(y[2], y[3]), T::pack(y[4], y[5]),

@@ -1,7 +1,11 @@
-"""What a row must not notice: the largest finite values of keys it does not see."""
+"""What a row or a channel must not notice: the largest finite values, and
+channels that are not turned beside ones that are not finite."""
+import math
+
 import pytest
 import torch
 
+from kv_cache_compression_cachegen_b200 import torch_api as ta
 from test_gpu_paged_paths import attend, build, reference
 from paged_util import check_close
 
@@ -26,3 +30,29 @@ def test_the_largest_values_of_keys_that_only_later_rows_see(D, dtype):
     want, tol = reference(b)
     out = attend(b).cpu()
     check_close(out[good], want[good], tol[good], "rows before the key")
+
+
+@pytest.mark.parametrize("inter,rot,D", [(1, 12, 16), (1, 2, 16), (1, 30, 64), (1, 14, 80),
+                                         (0, 12, 16), (0, 6, 32), (0, 26, 64)])
+def test_channels_behind_the_rotation_pass_unchanged(inter, rot, D):
+    # no norm: what is not turned comes out as it went in, whatever its neighbours hold
+    T, N, H = torch.float16, 9, 2
+    g = torch.Generator(device=DEV).manual_seed(rot)
+    x = torch.randn(N, 3 * H, D, generator=g, device=DEV).to(T)
+    x[1, :, rot + 1] = math.inf
+    x[2, :, rot] = -math.inf
+    x[3, :, rot:] = -0.0
+    x[4, :, rot + 1] = math.nan
+    pool = torch.zeros(1, 2, 2, 16, H, D, dtype=T, device=DEV)
+    q_out = torch.zeros(N, H, D, dtype=T, device=DEV)
+    call = ta.PagedAppend((1, H, D), H, T, DEV)
+    slots = torch.arange(N, device=DEV) + 5
+    positions = torch.arange(N, device=DEV, dtype=torch.int32) + 3
+    call.append(x[:, :H], x[:, H:2 * H], x[:, 2 * H:], q_out, pool, 0, positions, slots,
+                ta.rope_table(50, rot, DEV), interleaved=bool(inter))
+    torch.cuda.synchronize()
+    assert ta.status_of(call.status) == 0
+    got = torch.cat([q_out, pool[0, 0].view(-1, H, D)[slots]], 1)[..., rot:]
+    want = x[:, :2 * H, rot:]
+    same = (got.view(torch.int16) == want.view(torch.int16)) | (got.isnan() & want.isnan())
+    assert same.all(), (~same).nonzero()[0].tolist()
