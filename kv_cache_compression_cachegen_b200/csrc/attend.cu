@@ -150,12 +150,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(AttnParams p)
   if (row_id >= p.num_tokens * p.q_heads) return;
   const int t = row_id / p.q_heads, qh = row_id - t * p.q_heads;
   if (t >= p.q_starts[p.num_requests]) return;
-  int lo = 0, hi = p.num_requests - 1;  // the last request that starts at or before t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.q_starts[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
+  const int lo = last_not_above(p.num_requests, t, FirstRows{p.q_starts});
   Request req;
   if (!load_request(p, lo, req) || t < req.first || t >= req.first + req.tokens) return;
   const int head = div_of(qh, p.group_div), member = qh - head * p.group;

@@ -174,10 +174,7 @@ __device__ __forceinline__ int batch_rows(const AttnParams& p) {
 
 template <int kTile>
 __device__ __forceinline__ int slot_base(const AttnParams& p, int r) {
-  if (kTile == kRowTile) return r;
-  int a = p.q_starts[r];
-  a = a < 0 ? 0 : (a > p.num_tokens ? p.num_tokens : a);
-  return int(int64_t(a) * p.group / kTile) + r;
+  return kTile == kRowTile ? r : FirstSlots{p.q_starts, p.num_tokens, p.group, kTile}(r);
 }
 
 // What an item costs besides its units (queries, output, an empty pipeline), in
@@ -191,9 +188,8 @@ __host__ __device__ constexpr int item_cost() {
 }
 
 // The item of slot x and its units for each kv head; 0 where it holds no rows.
-// from: a request whose slots start at or before x, or -1 to search for one.
 template <int kTile, int kKeys>
-__device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it, int from = -1) {
+__device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it) {
   const int own = own_slots<kTile>(p);
   if (x >= own) {
     it.request = -1;
@@ -204,18 +200,8 @@ __device__ __forceinline__ int slot_item(const AttnParams& p, int x, Item& it, i
     it.row = (x - own) * kTile;
   } else {
     int lo = x;
-    if (kTile != kRowTile && from >= 0) {
-      lo = from;
-      while (lo + 1 < p.num_requests && slot_base<kTile>(p, lo + 1) <= x) ++lo;
-    } else if (kTile != kRowTile) {
-      lo = 0;
-      int hi = p.num_requests - 1;  // the last request whose slots start at or before x
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (slot_base<kTile>(p, mid) <= x) lo = mid;
-        else hi = mid - 1;
-      }
-    }
+    if (kTile != kRowTile)
+      lo = last_not_above(p.num_requests, x, FirstSlots{p.q_starts, p.num_tokens, p.group, kTile});
     it.request = lo;
     if (!load_request(p, lo, it.req)) {
       report(p.status, CG_ERR_MISMATCH);
@@ -392,8 +378,7 @@ struct Walk {
   __device__ __forceinline__ bool next(const AttnParams& p) {
     while (u < u_end && x < slots) {
       if (known != x) {
-        // slots are taken in order: the request is the last one's or soon behind
-        cost = slot_item<kTile, kKeys>(p, x, it, known >= 0 ? it.request : -1);
+        cost = slot_item<kTile, kKeys>(p, x, it);
         known = x;
       }
       if (cost == 0 || u >= (cum + cost) * p.kv_heads) {

@@ -34,4 +34,37 @@ CG_HOST_DEVICE int64_t share_of(int c, int64_t units, int ctas) {
   return units * c / ctas;
 }
 
+// The index that a bisection of [0, n) finds for the last one with at(i) <= x.
+// Where `at` does not rise all the way (lengths that a call should not have been
+// given) all users still find the same one, which is what matters: the line's
+// sums, the walks over it and the joins have to agree on a slot's request.
+template <typename At>
+CG_HOST_DEVICE int last_not_above(int n, int x, const At& at) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (at(mid) <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// First slots of requests whose rows begin at `starts` in a batch of `tokens`, in a
+// line of tiles of `tile` rows a kv head.
+struct FirstSlots {
+  const int32_t* starts;
+  int tokens, group, tile;
+  CG_HOST_DEVICE int operator()(int r) const {
+    int a = starts[r];
+    a = a < 0 ? 0 : (a > tokens ? tokens : a);
+    return int(int64_t(a) * group / tile) + r;
+  }
+};
+
+// First rows.
+struct FirstRows {
+  const int32_t* starts;
+  CG_HOST_DEVICE int operator()(int r) const { return starts[r]; }
+};
+
 }  // namespace cg

@@ -264,3 +264,28 @@ def test_nine_to_sixteen_rows_of_many_channels(dim, dtype):
     out = torch.empty_like(b["q"])
     call.run(b["q"], b["pool"], 0, b["starts"], b["lens"], b["tables"], 3, out, window=100)
     check_close(out, *reference(b, window=100))
+
+
+@pytest.mark.parametrize("prefix", [0, 100])
+def test_starts_out_of_order_leave_other_requests_alone(prefix):
+    # request 0 and the ones behind it claim the same rows and request 1 has none:
+    # the last one's rows are its own, and right
+    added, lens = [1500, 0, 30, 1440, 200], [2000, 5, 40, 1500, 700]
+    starts = [0, 1500, 30, 60, 1500, 1700]
+    b = build(lens, [0, 0, 0, 0, 200], 4, 2, 64, 16, torch.float16, prefix, seed=4)
+    want, tol = reference(b)
+    q = torch.zeros(1700, 4, 64, dtype=torch.float16, device=DEV)
+    q[1500:] = b["q"]
+    b.update(q=q, starts=torch.tensor(starts, dtype=torch.int32, device=DEV))
+    call = ta.PagedAttention((1, 2, 64), 4, q.dtype, 1700, 5, DEV)
+    call.reserve_shared()
+    call.workspace.fill_(255)
+    out = torch.empty_like(q)
+    args = (b["starts"], b["lens"], b["tables"], max(added), out)
+    if prefix:
+        call.run_shared(q, b["pool"], 0, b["prefix_table"], prefix, *args)
+    else:
+        call.run(q, b["pool"], 0, *args)
+    torch.cuda.synchronize()
+    assert ta.status_of(call.status) == 4  # CG_ERR_MISMATCH
+    check_close(out[1500:], want, tol)

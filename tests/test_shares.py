@@ -1,6 +1,7 @@
 """How the attention kernels deal a line of units to their CTAs, against plain
 integers.  The functions are the kernels' own, compiled for the host."""
 import ctypes
+import random
 import shutil
 import subprocess
 from pathlib import Path
@@ -20,6 +21,16 @@ extern "C" void owners(const int64_t* u, int n, int64_t units, int ctas, int* ou
 extern "C" int most_ctas() { return cg::kMaxRowCtas; }
 extern "C" int row_ctas_per_sm() { return cg::kRowCtasPerSm; }
 extern "C" int64_t narrow() { return cg::kNarrowUnits; }
+// the request that a join finds for row t, and the one of the slot that it takes
+extern "C" void agree(const int* q, int B, int tokens, int group, int tile, int t, int member,
+                      int* out) {
+  const int lo = cg::last_not_above(B, t, cg::FirstRows{q});
+  out[0] = lo;
+  const cg::FirstSlots slots{q, tokens, group, tile};
+  const int x = slots(lo) + ((t - q[lo]) * group + member) / tile;
+  out[1] = cg::last_not_above(B, x, slots);
+  out[2] = x;
+}
 """
 
 
@@ -67,3 +78,24 @@ def test_the_sizes_of_long_batches(lib, ctas, units):
 def test_the_narrow_arithmetic_fits_the_most_ctas(lib):
     assert lib.narrow() * lib.most_ctas() <= 1 << 32
     assert lib.most_ctas() == 160 * lib.row_ctas_per_sm()
+
+
+@pytest.mark.parametrize("rising", [True, False])
+def test_joins_and_slots_find_the_same_request(lib, rising):
+    # lengths out of order are a caller's mistake that must not lead a join astray
+    r = random.Random(int(rising))
+    out = (ctypes.c_int * 3)()
+    for _ in range(3000):
+        B, tokens = r.randint(1, 12), r.choice([40, 700, 5000])
+        group, tile = r.choice([1, 3, 4, 64]), r.choice([128, 256])
+        inside = [r.randint(0, tokens) for _ in range(B + 1)]
+        starts = sorted(inside) if rising else [x + r.choice([0, 0, -9000, 9000]) for x in inside]
+        q = (ctypes.c_int * (B + 1))(*starts)
+        for _ in range(20):
+            t, member = r.randrange(tokens), r.randrange(group)
+            lib.agree(q, B, tokens, group, tile, t, member, out)
+            first, last = starts[out[0]], starts[out[0] + 1]
+            if not 0 <= first <= t < last <= tokens:
+                continue  # the join leaves this row out
+            assert out[0] == out[1], (starts, t)
+            assert 0 <= out[2] < tokens * group // tile + B
