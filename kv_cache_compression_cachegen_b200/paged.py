@@ -9,9 +9,13 @@ behind a shared prefix.  Each object holds what a program keeps between calls
 math runs in libcachegen's kernels.  Nothing here synchronises: data errors go
 to ``status``, which the caller reads after synchronising
 (``torch_api.status_of``).  Work is queued on ``stream``, or on the current
-stream of the object's device; an object is used by one stream at a time.  Its
-own buffers may be used on any stream; the caller's tensors are the caller's to
-order and to keep, as everywhere in this package.
+stream of the object's device; an object is used by one stream, and one host
+thread, at a time.  Its own buffers may be used on any stream: one that is new
+to the object waits until they are made.  (A captured call does not wait:
+``torch.cuda.graph`` has waited for the device before it captures, and a
+program that begins a capture otherwise synchronises after making the object.)
+The caller's tensors are the caller's to order and to keep, as everywhere in
+this package.
 """
 from __future__ import annotations
 
@@ -41,6 +45,11 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _get_device = torch._C._cuda_getDevice
 
 
+def _capturing(stream: torch.cuda.Stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class _Call:
     """Device, value type, status word and launch of one object's calls."""
 
@@ -57,7 +66,9 @@ class _Call:
         self.status = (torch.zeros(1, dtype=torch.int32, device=self.device)
                        if status is None else status)
         self._status = self._vector(self.status, "status", torch.int32, 1)
-        self._seen = {_raw_stream(self._index)}  # streams that self._buffers() are known to
+        self._ready = None
+        self._buffers = ()
+        self._made(self.status)
 
     def _vector(self, t: torch.Tensor, name: str, dtype, count: int = 0) -> int:
         if t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous() or \
@@ -87,18 +98,29 @@ class _Call:
         raise ValueError("pool must be a contiguous [L, 2, num_pages, page_tokens, H, D] "
                          f"tensor of the object's type on {self.device}")
 
-    def _buffers(self) -> tuple:
-        """The object's own device buffers."""
-        return (self.status,)
+    def _made(self, *buffers: torch.Tensor) -> None:
+        """Add buffers that have been made on the current stream to the object's."""
+        self._buffers += buffers
+        here = torch.cuda.current_stream(self.device)
+        self._seen = set()  # streams that know the buffers
+        if not _capturing(here):  # a capture has memory of its own, which nothing still uses
+            self._ready = torch.cuda.Event()
+            self._ready.record(here)
+            self._seen.add(here.cuda_stream)
 
     def _meet(self, handle: int) -> None:
-        """Tell the caching allocator that a stream other than the one the
-        buffers were made on uses them, so that their memory is not handed out
-        again before that stream is done with them."""
+        """Have a stream that is new to the buffers wait until they are made
+        (their memory may come from work that is still queued), and tell the
+        caching allocator that it uses them, so that their memory is not handed
+        out again before that stream is done with them."""
         s = (torch.cuda.ExternalStream(handle, device=self.device) if handle
              else torch.cuda.default_stream(self.device))
-        for t in self._buffers():
+        for t in self._buffers:
             t.record_stream(s)
+        if _capturing(s):
+            return  # cannot wait for what is outside of its capture; met again later
+        if self._ready is not None:
+            s.wait_event(self._ready)
         self._seen.add(handle)
 
     def _launch(self, fn, stream, *args) -> None:
@@ -134,12 +156,10 @@ class PagedTables(_Call):
         self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=dev)
         self.positions = torch.full((max_tokens,), -1, dtype=torch.int32, device=dev)
         self.taken = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._made(self.kv_lens, self.q_starts, self.slots, self.positions, self.taken)
         self._args = ExtendArgs()
         self._ref = ctypes.byref(self._args)
         self._fn = library().cg_extend_tables
-
-    def _buffers(self) -> tuple:
-        return (self.status, self.kv_lens, self.q_starts, self.slots, self.positions, self.taken)
 
     def extend(self, held: torch.Tensor, added: torch.Tensor, block_tables: torch.Tensor,
                free_pages: torch.Tensor, taken: torch.Tensor | None = None,
@@ -168,6 +188,7 @@ def rope_table(max_positions: int, rot_dim: int, device, theta: float = 10000.0,
     """The [max_positions, rot_dim] table of PagedAppend: cosines, then sines."""
     call = _Call(device, None)
     out = torch.empty((max_positions, rot_dim), dtype=torch.float32, device=call.device)
+    call._made(out)
     call._launch(library().cg_rope_table, stream, max_positions, rot_dim, theta, out.data_ptr())
     return out
 
@@ -241,12 +262,13 @@ class PagedAttention(_Call):
         need = cg_attention_workspace_bytes(self.shape, self.num_q_heads, self.max_tokens,
                                             self.max_requests, shared)
         if self.workspace is None or self.workspace.numel() < need:
+            here = _raw_stream(self._index)
+            if here not in self._seen:
+                self._meet(here)
             self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            self._seen = {_raw_stream(self._index)}
+            self._buffers = (self.status,)
+            self._made(self.workspace)
         self._has_shared = shared
-
-    def _buffers(self) -> tuple:
-        return self.status, self.workspace
 
     def reserve_shared(self) -> None:
         """Size the workspace for run_shared now (its first call does so
