@@ -14,6 +14,8 @@ thread, at a time.  Its own buffers may be used on any stream: one that is new
 to the object waits until they are made.  (A captured call does not wait:
 ``torch.cuda.graph`` has waited for the device before it captures, and a
 program that begins a capture otherwise synchronises after making the object.)
+A graph that captured an object's calls uses its buffers: keep the object as
+long as the graph, and replay both in order as calls of one object are.
 The caller's tensors are the caller's to order and to keep, as everywhere in
 this package.
 """
@@ -255,7 +257,8 @@ class PagedAttention(_Call):
         self._refs = ctypes.byref(self.shape), ctypes.byref(self._args)
         self._fn, self._shared_fn = library().cg_attention_paged, library().cg_attention_shared
         self._scale = 1.0 / math.sqrt(self.shape.head_dim)
-        self.workspace = None
+        self.workspace = self._replaced = None
+        self._ran = False
         self._reserve(False)
 
     def _reserve(self, shared: bool) -> None:
@@ -265,6 +268,8 @@ class PagedAttention(_Call):
             here = _raw_stream(self._index)
             if here not in self._seen:
                 self._meet(here)
+            if self._ran:
+                self._replaced = self.workspace  # a captured call goes on using it
             self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
             self._buffers = (self.status,)
             self._made(self.workspace)
@@ -272,7 +277,8 @@ class PagedAttention(_Call):
 
     def reserve_shared(self) -> None:
         """Size the workspace for run_shared now (its first call does so
-        otherwise), for a program that captures its first call."""
+        otherwise), for a program that captures its first call, and before the
+        first run(), whose workspace would be kept beside the new one."""
         if not self._has_shared:
             self._reserve(True)
 
@@ -307,6 +313,7 @@ class PagedAttention(_Call):
         by default; lse: fp32 [N, Hq] that receives the log-sums."""
         self._set(q, pool, layer, q_starts, kv_lens, block_tables, max_q, out, window, sinks,
                   scale, lse)
+        self._ran = True
         self._launch(self._fn, stream, *self._refs)
         return out
 

@@ -138,3 +138,38 @@ def test_made_on_a_busy_stream_and_grown_on_another():
     assert ta.status_of(call.status) == 0
     want, _, tol = b.oracle()
     check_close(out, want, tol)
+
+
+def test_a_captured_call_keeps_its_workspace_when_a_larger_one_is_made():
+    # run() captured, then the first run_shared(): the graph still writes where it did
+    H, Hq, D, T = 2, 8, 128, torch.float16
+    b = Batch([3000, 700, 90], [1, 1, 1], Hq, H, D, 16, T, seed=3)
+    c = Batch([30, 64, 5], [1, 1, 1], Hq, H, D, 16, T, seed=4, prefix=160)
+    q, pool, starts, lens, tables, _ = b.device()
+    q2, pool2, starts2, lens2, tables2, ptable = c.device()
+    call = ta.PagedAttention((1, H, D), Hq, T, 3, 3, DEV)
+    out, out2 = torch.empty_like(q), torch.empty_like(q2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.run(q, pool, 0, starts, lens, tables, 1, out)
+    size, first = call.workspace.numel(), call.workspace.data_ptr()
+    call.run_shared(q2, pool2, 0, ptable, 160, starts2, lens2, tables2, 1, out2)
+    assert call.workspace.data_ptr() != first
+    others = [torch.full((size,), 255, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert ta.status_of(call.status) == 0
+    assert all(bool((x == 255).all()) for x in others)
+    want, _, tol = b.oracle()
+    check_close(out, want, tol)
+    want, _, tol = c.oracle()
+    check_close(out2, want, tol)
+
+
+def test_an_unused_workspace_is_not_kept():
+    call = ta.PagedAttention((1, 2, 128), 8, torch.float16, 3, 3, DEV)
+    torch.cuda.synchronize()
+    held, old = torch.cuda.memory_allocated(), call.workspace.numel()
+    call.reserve_shared()
+    assert torch.cuda.memory_allocated() - held < call.workspace.numel() - old + (4 << 20)
