@@ -2,6 +2,7 @@
 // the join of what several CTAs computed of one row.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "attend.cuh"
 
@@ -297,7 +298,10 @@ cudaError_t launch_attention(const cg_attention_args& a, const cg_shape& s,
   p.shared = shared;
   // a negative scale is the positive one with q's signs turned, so that the
   // largest product is the largest score
-  p.scale_log2 = std::fabs(a.scale) * 1.44269504089f;
+  // (a scale of zero is the smallest number, so that a hidden score, -infinity, stays
+  // that: scores are zero to within 2^-20 all the same)
+  p.scale_log2 = std::max(std::fabs(a.scale) * 1.44269504089f,
+                          std::numeric_limits<float>::denorm_min());
   p.q_flip = std::signbit(a.scale) ? 0x80008000u : 0u;
   p.prefix_small = int64_t(p.num_tokens) * p.group <= kRowTile;
   p.tiled = int64_t(p.max_q) * p.group > kRowTile && !p.prefix_small;

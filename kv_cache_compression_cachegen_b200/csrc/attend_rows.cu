@@ -78,13 +78,13 @@ __global__ void __launch_bounds__(kThreads, Shape<DC, NR>::kCtasPerSm)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[2 * S::kStages];
   __shared__ uint32_t no_page[kNoted][4];
-  __shared__ int dead_mem;
+  __shared__ int dead_mem[2];
   __shared__ float stat_m[kWarps][16], stat_l[kWarps][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   float* join = reinterpret_cast<float*>(smem_raw + (base - smem_addr(smem_raw)) +
                                          S::kStages * S::kStage);
-  Ring ring{base, smem_addr(bars), smem_addr(bars) + 8 * S::kStages, no_page, &dead_mem};
+  Ring ring{base, smem_addr(bars), smem_addr(bars) + 8 * S::kStages, no_page, dead_mem};
 
   let_next_start();
   if (threadIdx.x == 32 * kWarps && maps.box > 0) {
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DC, NR>::kCtasPerSm)
     prefetch_map(&maps.v);
   }
   if (threadIdx.x == 0) {
-    dead_mem = 0;
+    dead_mem[0] = dead_mem[1] = 0;
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(ring.full + 8 * i, kLoadWarps);
       mbar_init(ring.empty + 8 * i, kWarps);

@@ -110,88 +110,243 @@ __device__ __forceinline__ uint32_t below(int n) {
   return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
 }
 
-// A row that met a value which is not finite, computed again by a warp from
-// the definition: a masked key's weight of zero does not hide an infinity or a
-// NaN in the matrix product.  o: four channels a lane and 128 channels apart.
-template <typename T>
-__device__ __forceinline__ void recompute_row(const AttnParams& p, const Deal& it, int row,
-                                              int kKeys, float (&o)[2][4], float& m, float& l) {
+// A weight of zero does not hide an infinity or a NaN in the matrix product.  Of a
+// warp's rows whose outputs are not finite (`odd` lanes; a lane's row stands at
+// `pos`), those that a value which is not finite and which they do not see has met,
+// a bit each: only these are computed again.  The others' own keys made them so,
+// all rows behind one bad token perhaps.
+template <typename T, int kKeys>
+__device__ __forceinline__ uint32_t rows_met(const AttnParams& p, const Deal& it, int pos,
+                                             bool odd) {
+  const int lane = threadIdx.x & 31;
+  const bool prefix = it.request < 0;
+  const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
+  const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
+  const int p0 = prefix ? it.row0 : it.row0 + div_of(it.row, p.group_div);
+  const int p1 = prefix ? it.row0 : it.row0 + div_of(it.row + it.rows - 1, p.group_div);
+  const Span span = span_of<kKeys>(p0, p1, window, sinks);  // outside of it zeros were loaded
+  const int64_t step = int64_t(p.kv_heads) * p.dim;
+  const int past = window == 0 ? 0 : int(max(0ll, (long long)pos - window + 1));
+  bool met = false;
+  for (int u = it.first; u < it.last; ++u) {
+    const int key0 = unit_key<kKeys>(span, u), end = key0 + kKeys - 1;
+    const bool whole = end <= pos && (window == 0 || pos - key0 < window || end < sinks);
+    if (__all_sync(~0u, !odd || met || whole)) continue;
+    for (int from = key0; from < key0 + kKeys; from += 32) {
+      const int key = from + lane;
+      const int at = key < span.hi && (key >= span.lo || key < span.sink_end)
+                         ? pool_row(p, table, key)
+                         : -1;
+      bool bad = false;
+      if (at >= 0) {
+        const uint16_t* v = p.v_pool + at * step + int64_t(it.head) * p.dim;
+#pragma unroll 4
+        for (int d = 0; d < p.dim; d += 8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + d);
+          bad |= T::not_finite(x.x) | T::not_finite(x.y) | T::not_finite(x.z) | T::not_finite(x.w);
+        }
+      }
+      const uint32_t seen = below(pos + 1 - from) & (~below(past - from) | below(sinks - from));
+      met |= (__ballot_sync(~0u, bad) & ~seen) != 0;
+    }
+  }
+  return __ballot_sync(~0u, odd && met);
+}
+
+// Rows computed again by a warp from the definition, kRedo at a time, which share
+// the loads of K and V: rows[i] of the item, at[i] its position.  A lane has a key's
+// scores, and four channels of each row's output, 128 channels apart.  `beat` counts
+// on, for those who wait meanwhile.  40 requests of 20,000 keys, 4 kv heads of 64
+// under two, 120 rows of each head before a bad value: 84 ms; one at a time 114.
+// Four take 62, but with registers that the usual way then spills (chunks 5 % longer).
+constexpr int kRedo = 2;
+template <typename T, int kKeys>
+__device__ __forceinline__ void recompute_rows(const AttnParams& p, const Deal& it,
+                                               const int (&rows)[kRedo], const int (&at)[kRedo],
+                                               int* beat, float (&o)[kRedo][2][4],
+                                               float (&m)[kRedo], float (&l)[kRedo]) {
   const int lane = threadIdx.x & 31, head = it.head;
   const bool prefix = it.request < 0;
   const int32_t* table = prefix ? p.prefix_table : p.tables + int64_t(it.request) * p.max_pages;
   const int window = prefix ? 0 : p.window, sinks = prefix ? 0 : p.sinks;
-  const int tok = div_of(row, p.group_div), at = prefix ? it.row0 : it.row0 + tok;
-  const uint16_t* q = p.q + int64_t(it.token0 + tok) * p.q_stride +
-                      int64_t(head * p.group + row - tok * p.group) * p.dim;
+  const uint16_t* q[kRedo];
+#pragma unroll
+  for (int i = 0; i < kRedo; ++i) {
+    const int tok = div_of(rows[i], p.group_div);
+    q[i] = p.q + int64_t(it.token0 + tok) * p.q_stride +
+           int64_t(head * p.group + rows[i] - tok * p.group) * p.dim;
+    m[i] = kNegInf;
+    l[i] = 0.f;  // of this lane's keys
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][h][e] = 0.f;
+  }
   const int64_t step = int64_t(p.kv_heads) * p.dim;
-  m = kNegInf;
-  l = 0.f;
-  for (int h = 0; h < 2; ++h)
-    for (int e = 0; e < 4; ++e) o[h][e] = 0.f;
+  const auto eight = [](uint4 v, float2 (&f)[4]) {
+    f[0] = T::unpack(v.x), f[1] = T::unpack(v.y), f[2] = T::unpack(v.z), f[3] = T::unpack(v.w);
+  };
   for (int u = it.first; u < it.last; ++u) {
     const int unit = u < it.sink_units ? u : it.first_unit + u - it.sink_units;
     for (int k0 = 0; k0 < kKeys; k0 += 32) {
       const int key = unit * kKeys + k0 + lane;
-      int from = -1;
-      if (sees(key, at, window, sinks)) from = pool_row(p, table, key);
-      float s = kNegInf;
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < kRedo; ++i) any |= sees(key, at[i], window, sinks);
+      const int from = any ? pool_row(p, table, key) : -1;
+      if (__all_sync(~0u, from < 0)) continue;
+      float s[kRedo], w[kRedo];
+#pragma unroll
+      for (int i = 0; i < kRedo; ++i) s[i] = 0.f;
       if (from >= 0) {
         const uint16_t* k = p.k_pool + from * step + int64_t(head) * p.dim;
-        float dot = 0.f;
-        for (int d = 0; d < p.dim; d += 2) {
-          const float2 a = T::unpack(*reinterpret_cast<const uint32_t*>(q + d) ^ p.q_flip);
-          const float2 b = T::unpack(*reinterpret_cast<const uint32_t*>(k + d));
-          dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
-        }
-        s = dot * p.scale_log2;
-      }
-      float top = s;
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-      top = fmaxf(top, m);
-      const float f = weight_of(m, top);
-      m = top;
-      l *= f;
-      for (int h = 0; h < 2; ++h)
-        for (int e = 0; e < 4; ++e) o[h][e] *= f;
-      const float w = s == kNegInf ? 0.f : exp2_fast(s - m);
-      for (int j = 0; j < 32; ++j) {
-        const int src = __shfl_sync(~0u, from, j);
-        const float wj = __shfl_sync(~0u, w, j);
-        if (src < 0) continue;
-        l += wj;
-        const uint16_t* v = p.v_pool + src * step + int64_t(head) * p.dim;
-        for (int h = 0; h < 2; ++h)
-          if (128 * h + 4 * lane < p.dim) {
-            const uint2 x = *reinterpret_cast<const uint2*>(v + 128 * h + 4 * lane);
-            const float2 a = T::unpack(x.x), b = T::unpack(x.y);
-            o[h][0] = fmaf(wj, a.x, o[h][0]);
-            o[h][1] = fmaf(wj, a.y, o[h][1]);
-            o[h][2] = fmaf(wj, b.x, o[h][2]);
-            o[h][3] = fmaf(wj, b.y, o[h][3]);
+#pragma unroll 2
+        for (int d = 0; d < p.dim; d += 8) {
+          float2 a[4], b[4];
+          eight(*reinterpret_cast<const uint4*>(k + d), b);
+#pragma unroll
+          for (int i = 0; i < kRedo; ++i) {
+            uint4 x = *reinterpret_cast<const uint4*>(q[i] + d);
+            x.x ^= p.q_flip, x.y ^= p.q_flip, x.z ^= p.q_flip, x.w ^= p.q_flip;
+            eight(x, a);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[i] = fmaf(a[c].x, b[c].x, fmaf(a[c].y, b[c].y, s[i]));
           }
+        }
+      }
+      uint32_t seen[kRedo];
+#pragma unroll
+      for (int i = 0; i < kRedo; ++i) {
+        const bool mine = from >= 0 && sees(key, at[i], window, sinks);
+        seen[i] = __ballot_sync(~0u, mine);
+        s[i] = mine ? s[i] * p.scale_log2 : kNegInf;
+        float top = s[i];
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+        top = fmaxf(top, m[i]);
+        const float f = weight_of(m[i], top);
+        m[i] = top;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][h][e] *= f;
+        w[i] = s[i] == kNegInf ? 0.f : exp2_fast(s[i] - top);
+        l[i] = l[i] * f + w[i];
+      }
+#pragma unroll 1
+      for (int j0 = 0; j0 < 32; j0 += 4) {
+        uint2 x[4][2];  // the values of four keys on their way together
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int src = __shfl_sync(~0u, from, j0 + j);
+          const uint16_t* v = p.v_pool + src * step + int64_t(head) * p.dim + 4 * lane;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            x[j][h] = make_uint2(0, 0);
+            if (src >= 0 && 128 * h + 4 * lane < p.dim)
+              x[j][h] = *reinterpret_cast<const uint2*>(v + 128 * h);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < kRedo; ++i) {
+            const float wj = __shfl_sync(~0u, w[i], j0 + j);
+            if (!((seen[i] >> (j0 + j)) & 1)) continue;  // the same for the whole warp
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (128 * h >= p.dim) break;
+              const float2 a = T::unpack(x[j][h].x), b = T::unpack(x[j][h].y);
+              o[i][h][0] = fmaf(wj, a.x, o[i][h][0]);
+              o[i][h][1] = fmaf(wj, a.y, o[i][h][1]);
+              o[i][h][2] = fmaf(wj, b.x, o[i][h][2]);
+              o[i][h][3] = fmaf(wj, b.y, o[i][h][3]);
+            }
+          }
+      }
+      if (lane == 0) atomicAdd(beat, 1);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRedo; ++i)
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l[i] += __shfl_xor_sync(~0u, l[i], x);
+}
+
+// Of a warp's 32 rows from `first` on, those named in `maybe`: see rows_met.  Not
+// inlined: the few registers and instructions of the usual way stay together.
+template <typename T, int kRows, int kKeys>
+__device__ __noinline__ void redo_rows(const AttnParams& p, const Deal& it, int first,
+                                       uint32_t maybe, int* beat) {
+  const int lane = threadIdx.x & 31, D = p.dim;
+  const bool prefix = it.request < 0, direct = it.whole && !p.shared;
+  const int mine = it.row + min(first + lane, it.rows - 1);
+  const int pos = prefix ? it.row0 : it.row0 + div_of(mine, p.group_div);
+  uint32_t again = rows_met<T, kKeys>(p, it, pos, (maybe >> lane) & 1);
+  __syncwarp();  // what other lanes have stored of these rows comes before
+  while (again) {
+    int rows[kRedo], at[kRedo];
+    uint32_t here = 0;  // which of them there are
+#pragma unroll
+    for (int i = 0; i < kRedo; ++i) {
+      rows[i] = i > 0 && again == 0 ? rows[0] : it.row + first + __ffs(again) - 1;
+      at[i] = prefix ? it.row0 : it.row0 + div_of(rows[i], p.group_div);
+      if (again != 0) here |= 1u << i;
+      again &= again - 1;
+    }
+    float o[kRedo][2][4], m[kRedo], l[kRedo];
+    recompute_rows<T, kKeys>(p, it, rows, at, beat, o, m, l);
+#pragma unroll
+    for (int i = 0; i < kRedo; ++i) {
+      if (!((here >> i) & 1)) continue;
+      const int tok = div_of(rows[i], p.group_div);
+      const int64_t t = it.token0 + tok;
+      const int qh = it.head * p.group + rows[i] - tok * p.group;
+      const int64_t piece = int64_t(it.piece) * kRows + rows[i] - it.row;
+      const int64_t whole = (int64_t(prefix) * p.num_tokens + t) * p.q_heads + qh;
+      const float scale = direct ? (l[i] == 0.f ? 0.f : 1.f / l[i]) : 1.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int d = 128 * h + 4 * lane;
+        if (d >= D) continue;
+        const float(&v)[4] = o[i][h];
+        if (direct)
+          *reinterpret_cast<uint2*>(p.out + t * p.out_stride + int64_t(qh) * D + d) = make_uint2(
+              T::pack(v[0] * scale, v[1] * scale), T::pack(v[2] * scale, v[3] * scale));
+        else
+          *reinterpret_cast<float4*>(
+              (it.whole ? p.whole + whole * D : p.tiles.pieces + piece * D) + d) =
+              make_float4(v[0], v[1], v[2], v[3]);
+      }
+      if (lane == 0) {
+        if (!direct)
+          (it.whole ? p.whole_stats[whole] : p.tiles.stats[piece]) = make_float2(m[i], l[i]);
+        else if (p.lse != nullptr)
+          p.lse[t * p.q_heads + qh] = log_sum(m[i], l[i]);
       }
     }
   }
+  __syncwarp();
 }
 
 template <typename T, int DC>
 __global__ void __launch_bounds__(kThreads, 1)
-    tile_kernel(AttnParams p, const __grid_constant__ KvMaps maps,
+    tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ KvMaps maps,
                 const __grid_constant__ CUtensorMap q_map, int by_map) {
   using G = Geometry<DC>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars_mem[2 * G::kStages + 12 + 2 * kItems];
   __shared__ Deal deals[kItems];
   __shared__ uint32_t tmem_slot;
-  __shared__ int dead_mem;
+  __shared__ int dead_mem[2];
   __shared__ __align__(16) uint32_t no_page[kNoted][4];
   const int warp = __shfl_sync(~0u, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t q_smem = base;
   const uint32_t kv_smem = base + G::kTiles * DC * G::kQBytes;
-  volatile int* dead = &dead_mem;
+  volatile int* dead = dead_mem;
   const uint32_t bars = smem_addr(bars_mem);
-  const Ring ring{kv_smem, bars, bars + 8 * G::kStages, no_page, &dead_mem};
+  const Ring ring{kv_smem, bars, bars + 8 * G::kStages, no_page, dead_mem};
   Bars bar;
   bar.q_full = ring.empty + 8 * G::kStages;
   bar.q_free = bar.q_full + 16;
@@ -208,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 32 * kQueryWarp && by_map) prefetch_map(&q_map);
   if (threadIdx.x == 0) {
-    dead_mem = 0;
+    dead_mem[0] = dead_mem[1] = 0;
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(ring.full + 8 * i, kLoadWarps);
       mbar_init(ring.empty + 8 * i, 1);
@@ -454,34 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!direct) (it.whole ? p.whole_stats[whole] : p.tiles.stats[piece]) = make_float2(m, l);
         else if (p.lse != nullptr) p.lse[t * p.q_heads + qh] = log_sum(m, l);
       }
-      // rows whose sums are not finite, where some keys were hidden
-      uint32_t again = __ballot_sync(~0u, real && mixed && odd);
-      __syncwarp();
-      while (again) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        const int rr = 128 * tile + 32 * (warp & 3) + src;
-        float o[2][4], mm, ll;
-        recompute_row<T>(p, it, it.row + rr, G::kKeys, o, mm, ll);
-        const float scale = direct ? (ll == 0.f ? 0.f : 1.f / ll) : 1.f;
-        const int64_t t2 = __shfl_sync(~0u, t, src);
-        const int qh2 = __shfl_sync(~0u, qh, src);
-        const int64_t whole2 = __shfl_sync(~0u, whole, src), piece2 = __shfl_sync(~0u, piece, src);
-        for (int h = 0; h < 2; ++h) {
-          const int d = 128 * h + 4 * lane;
-          if (d >= D) continue;
-          if (direct)
-            *reinterpret_cast<uint2*>(p.out + t2 * p.out_stride + int64_t(qh2) * D + d) = make_uint2(
-                T::pack(o[h][0] * scale, o[h][1] * scale), T::pack(o[h][2] * scale, o[h][3] * scale));
-          else
-            *reinterpret_cast<float4*>((it.whole ? p.whole + whole2 * D : p.tiles.pieces + piece2 * D) +
-                                       d) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
-        }
-        if (lane == 0) {
-          if (!direct) (it.whole ? p.whole_stats[whole2] : p.tiles.stats[piece2]) = make_float2(mm, ll);
-          else if (p.lse != nullptr) p.lse[t2 * p.q_heads + qh2] = log_sum(mm, ll);
-        }
-      }
+      // rows whose outputs are not finite, where some keys were hidden (a sum of weights
+      // that is not finite makes all of the row so, and comes of keys that it sees)
+      const uint32_t maybe = __ballot_sync(~0u, real && mixed && odd && l - l == 0.f);
+      if (maybe != 0)
+        redo_rows<T, G::kRows, G::kKeys>(p, it, 128 * tile + 32 * (warp & 3), maybe, dead_mem + 1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.item_free + 8 * (n % kItems));

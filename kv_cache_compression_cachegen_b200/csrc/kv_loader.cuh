@@ -28,7 +28,7 @@ struct Ring {
   // kNoted: a unit's note is written over when the stage of the unit kNoted behind
   // it is free, which at up to twelve stages is after the unit was read.
   uint32_t (*no_page)[4];
-  volatile int* dead;
+  volatile int* dead;  // and the beat behind it: mbar_wait's state
 };
 
 // DC: 64-channel blocks of a head.  wk: 0 or 1, which of the two warps.  False

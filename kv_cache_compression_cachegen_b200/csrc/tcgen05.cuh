@@ -21,10 +21,12 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 
 // Wait for the phase with this parity to complete.  Bounded: after about two
-// seconds, or when another thread of the CTA has given up, it sets *dead and
-// returns false.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+// seconds without a beat (state[1], which a thread with much to do by itself
+// counts up), or when another thread of the CTA has given up, it sets state[0]
+// and returns false.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* state) {
   long long start = 0;
+  int beat = 0;
   for (int i = 0;; ++i) {
     uint32_t done;
     asm volatile(
@@ -36,10 +38,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         : "memory");
     if (done) return true;
     if ((i & 63) == 63) {
-      if (start == 0) start = clock64();
-      if (*dead != 0) return false;
+      if (start == 0 || state[1] != beat) start = clock64(), beat = state[1];
+      if (state[0] != 0) return false;
       if (clock64() - start > 4000000000ll) {
-        *dead = 1;
+        state[0] = 1;
         return false;
       }
     }
