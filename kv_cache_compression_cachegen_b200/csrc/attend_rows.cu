@@ -423,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DC, NR>::kCtasPerSm)
     }
     if (!ok && lane == 0) report(p.status, CG_ERR_CUDA);
   }
+  __syncthreads();
+  let_settle(ring.dead);
   // this kernel may have started before the tile kernel was done; the join
   // waits for this one, and so for both
   wait_for_previous();

@@ -780,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  let_settle(dead);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);

@@ -48,6 +48,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// On the way out after a wait ran out (state[0]; behind a barrier of the CTA): a tenth
+// of a second, in which copies and products that are still under way complete and do
+// not write to memory that has been given back.
+__device__ __forceinline__ void let_settle(const volatile int* state) {
+  if (state[0] == 0) return;
+  const long long start = clock64();
+  while (clock64() - start < 200000000ll) __nanosleep(10000);
+}
+
 // ---- ordering between the proxies
 
 __device__ __forceinline__ void fence_async_smem() {
