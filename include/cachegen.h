@@ -384,6 +384,8 @@ cg_status cg_encode_static(const cg_shape* shape, const uint16_t* kv_dev, int64_
  * the row's heads * D; a token's heads are contiguous.
  * The arithmetic is fp32; values are rounded to the pool's type when they are
  * stored (and the weights of a softmax for the matrix product that uses them).
+ * A row of attention is divided by its sum of weights (2^8 each at most) at the
+ * end, so bf16 values from 2^120 over the number of keys on can give infinities.
  * Indexes and lengths are checked on the device before they are used; what a
  * bad one reaches is left out and CG_ERR_MISMATCH reported. */
 

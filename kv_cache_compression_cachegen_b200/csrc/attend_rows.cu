@@ -36,7 +36,8 @@ struct Shape {
   // Two CTAs an SM, but one where sixteen rows have more than 128 channels: 168
   // registers a thread hold neither those rows' sums nor their queries.  14 requests
   // of 113 keys, 32 kv heads of 256 under 16 rows each: 70 us against 91 with two;
-  // of 5,001 keys 823 against 1,083.
+  // of 5,001 keys 823 against 1,083.  (Sixteen rows of 65 to 128 channels spill 150
+  // bytes at two CTAs, and more than 128 channels 72 at eight rows and 322 at sixteen.)
   static constexpr int kCtasPerSm = row_ctas_per_sm(64 * DC, 8 * NR);
   static constexpr int kStages = (DC == 4 ? 3 : (DC == 2 ? 6 : 12)) * kRowCtasPerSm / kCtasPerSm;
   static constexpr int kStage = DC * kRowKeys * 128;
